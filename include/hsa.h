@@ -438,6 +438,180 @@ hsa_status hsa_step_cond(hsa_ctx* ctx, const hsa_model_weights* w, const hsa_sta
                          const hsa_cond* cond, int i, float sigma_i, float sigma_next,
                          int regroup);
 
+/* ------------------------------------------------------------------------
+ * Operators around the block for models that need them: 8-bit integer
+ * products, rotary positions, query/key norms, and cross-attention of ragged
+ * sequences.  The pages describe none of these; the formulas are given at each
+ * call.  Besides the conventions above:
+ *  - The calls below make the context's device current while they launch, so
+ *    they work from a thread whose current device is another one.
+ *  - They read no tensor on the host and never wait, so they can be captured
+ *    into a CUDA graph.  hsa_cross_attention uses the context's scratch: like
+ *    calls, replays of graphs captured from one context must not overlap.
+ *  - `ld_*` arguments are distances between rows in elements.
+ *  - n == 0 rows launch nothing.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the calls that take more than one. */
+typedef enum { HSA_BF16 = 0, HSA_F32 = 1 } hsa_type;
+
+/*
+ * Quantise n rows to signed 8 bits, one scale per row:
+ *   top = max_k |a[m,k]|;  scale[m] = top / 127;  q[m,k] = rint(a[m,k] * (127 / top))
+ * in fp32, halves to even, so |q| <= 127 and a ~ scale q.  A row with
+ * top < 2^-100 gives q = 0, scale = 0; a row that holds an infinity or a NaN
+ * gives q = 0, scale = NaN.
+ *   a     (device) HSA_BF16 or HSA_F32 [n, Kd], rows ld_a >= Kd apart (any alignment of rows);
+ *   q     (device) int8 [n, Kd] out, rows ld_q apart, a multiple of 16, >= Kd (bytes past Kd
+ *         are left as they are);
+ *   scale (device) fp32 [n] out.   1 <= Kd <= 131071.
+ * Weights kept in 8 bits are made by the same call (a row per output channel).
+ */
+hsa_status hsa_quant_rows(hsa_ctx* ctx, const void* a, int a_type, int n, int Kd, int64_t ld_a,
+                          int8_t* q, int64_t ld_q, float* scale);
+
+/*
+ * Linear map of 8-bit rows with scales per row and per output channel:
+ *   out[m,j] = a_scale[m] * w_scale[j] * sum_k a[m,k] w[j,k]
+ * The sum is exact (32-bit integers); the products are fp32, rounded once to bf16.
+ *   a (device) int8 [M, ld_a];  a_scale (device) fp32 [M];
+ *   w (device) int8 [Ncols, ld_w];  w_scale (device) fp32 [Ncols];
+ *   out (device) bf16 [M, Ncols].
+ *   ld_a, ld_w multiples of 16, >= Kd; bytes past Kd are ignored.
+ *   M >= 0, Ncols >= 1, 1 <= Kd <= 131071.
+ */
+hsa_status hsa_linear_quant(hsa_ctx* ctx, const int8_t* a, int64_t ld_a, const float* a_scale,
+                            int M, int Kd, const int8_t* w, int64_t ld_w, const float* w_scale,
+                            int Ncols, void* out);
+
+/*
+ * hsa_ln_gather_mod straight to 8 bits: the rows u[m] = LN(x[idx[m]]) (1 + mscale) + shift
+ * (fp32, not rounded to bf16 first) quantised as hsa_quant_rows does.
+ *   x, idx, n, shift, mscale as hsa_ln_gather_mod;  q (device) int8 [n, D] out;
+ *   scale (device) fp32 [n] out.  D <= 5120 (HSA_ERR_SHAPE beyond).
+ */
+hsa_status hsa_ln_gather_quant(hsa_ctx* ctx, const float* x, const int32_t* idx, int n, int8_t* q,
+                               float* scale, const float* shift, const float* mscale);
+
+/* Which places of a head form plane i of a rotation over `rot` places. */
+typedef enum {
+  HSA_ROPE_INTERLEAVED = 0, /* (2i, 2i + 1) */
+  HSA_ROPE_HALF = 1         /* (i, i + rot / 2) */
+} hsa_rope_layout;
+
+/* How frequencies are scaled for contexts longer than the model was trained on. */
+typedef enum {
+  HSA_ROPE_PLAIN = 0,  /* f_i = base^(-2 i / dim) */
+  HSA_ROPE_LINEAR = 1, /* f_i / factor (positions interpolated) */
+  HSA_ROPE_BASE = 2,   /* base * factor^(dim / (dim - 2)) in place of base (dim > 2) */
+  HSA_ROPE_PARTS = 3   /* by the turns r = orig_len f_i / 2 pi of a plane over the trained
+                          length: f_i / factor for r <= slow, f_i for r >= fast, and their
+                          mean weighted by (r - slow) / (fast - slow) in between */
+} hsa_rope_scaling;
+
+/* A rotary table: up to three position axes (e.g. frame, row, column of a
+ * video token), axis x turning dims[x] / 2 planes of its own, in axis order.
+ * Each axis has frequencies over its own dims[x]. */
+typedef struct {
+  int n_axes;      /* 1..3 */
+  int dims[3];     /* rotated places per axis: even, >= 2; their sum rot is <= 128 */
+  double base;     /* > 1 */
+  int scaling;     /* hsa_rope_scaling */
+  double factor;   /* >= 1; not read by HSA_ROPE_PLAIN */
+  double orig_len; /* > 0, HSA_ROPE_PARTS */
+  double fast, slow; /* fast > slow >= 0, HSA_ROPE_PARTS */
+  double amp;      /* multiplies cosines and sines (1: a pure rotation) */
+} hsa_rope_cfg;
+
+/*
+ * Table of a rotary position embedding: table[p][i] = amp (cos, sin)(pos[p][axis(i)] f_i).
+ * Angles are reduced in 64 bits, so far positions keep full fp32 accuracy.
+ *   cfg (host);  pos (device) int32 [P, n_axes], or NULL with one axis: row p has position p;
+ *   table (device) fp32 [P, rot / 2, 2] out.   P >= 0.
+ */
+hsa_status hsa_rope_table(hsa_ctx* ctx, const hsa_rope_cfg* cfg, const int32_t* pos, int P,
+                          float* table);
+
+/*
+ * Rotate the first `rot` places of every head: with (u, v) plane i of a head of
+ * row m and (c, s) = table[pos[m]][i],
+ *   out = (u c - v s, v c + u s),  or with `inverse` (u c + v s, v c - u s),
+ * the other places of the head copied.  The inverse is also the gradient.
+ *   x, out (device) type HSA_BF16 or HSA_F32, n rows of `heads` heads of D/H places, rows
+ *   ld_x / ld_out apart (multiples of 16 bytes); out may be x;
+ *   table (device) fp32 [P, rot / 2, 2];  pos (device) int32 [n] table rows, or NULL: row m
+ *   uses table row m;  rot a multiple of 16, 16 <= rot <= D/H;  heads >= 1.
+ * A row whose table row is outside [0, P) is left unwritten and reported by
+ * hsa_sync_check (HSA_ERR_DEVICE_CHECK).
+ */
+hsa_status hsa_rope(hsa_ctx* ctx, const void* x, int64_t ld_x, int type, int n, int heads,
+                    const float* table, int P, int rot, const int32_t* pos, int layout,
+                    int inverse, void* out, int64_t ld_out);
+
+/* What the RMS norm of queries and keys runs over. */
+typedef enum { HSA_NORM_NONE = 0, HSA_NORM_HEAD = 1, HSA_NORM_ROW = 2 } hsa_qk_norm;
+
+typedef struct {
+  int norm;           /* hsa_qk_norm: each head's D/H places, or the row's D */
+  const float* w_q;   /* (device) fp32 [D/H] (HEAD) or [D] (ROW) weights, NULL: 1 */
+  const float* w_k;   /* same, keys */
+  float eps;          /* x / sqrt(mean(x^2) + eps) * w;  >= 0 */
+  const float* table; /* (device) fp32 [P, rot / 2, 2], NULL: no rotation */
+  int P;              /* table rows */
+  int rot;            /* as hsa_rope */
+  int layout;         /* hsa_rope_layout */
+} hsa_qk_rope;
+
+/*
+ * Norm and rotation of fresh queries and keys, and the cache write, in one pass:
+ *   q[m]              = rot(norm(q_in[m]))
+ *   k_cache[idx[m]]   = rot(norm(k_in[m]))
+ *   v_cache[idx[m]]   = v_in[m]
+ * norm then rotation in fp32, rounded once to bf16.
+ *   idx (device) int32 [n] distinct cache rows in [0, N), or NULL: row m;
+ *   pos (device) int32 [n] table rows, or NULL: the cache row (a token's place in the latent);
+ *   q (device) bf16 [n, D] out, NULL: no queries;  q_in (device) bf16, rows ld_q apart, NULL: q in place;
+ *   k_cache (device) bf16 [N, D], NULL: no keys;   k_in (device) bf16, rows ld_k apart, NULL: the
+ *   cache rows in place (after hsa_qkv_project; idx must then ascend);
+ *   v_cache (device) bf16 [N, D] and v_in, rows ld_v apart: both or neither.
+ *   ld_* multiples of 8, >= D; 0 <= n <= N; D <= 10240 (HSA_ERR_SHAPE beyond).
+ * q may be q_in; no other output may overlap an input.  A row with an index or table row out of range
+ * (or, in place, an index not above the one before it) is skipped, its q row
+ * zeroed if that was to be written, and reported by hsa_sync_check.
+ */
+hsa_status hsa_qk_norm_rope(hsa_ctx* ctx, const hsa_qk_rope* a, const int32_t* idx,
+                            const int32_t* pos, int n, const void* q_in, int64_t ld_q, void* q,
+                            const void* k_in, int64_t ld_k, void* k_cache, const void* v_in,
+                            int64_t ld_v, void* v_cache);
+
+/* Cross-attention of B sequences of queries to B padded sequences of encoder states. */
+typedef struct {
+  const void* q;           /* (device) bf16 [n, D]: the sequences' queries one after another */
+  const int32_t* q_start;  /* (device) int32 [B + 1], ascending, in [0, n]: sequence b owns rows
+                              q_start[b] .. q_start[b + 1] - 1 */
+  int n, B;                /* n >= 0, B >= 1 */
+  const void* k;           /* (device) bf16 [B, S, kv_heads * D/H], rows ld_k apart, */
+  const void* v;           /*   sequences bs_k apart (elements); v likewise */
+  int64_t ld_k, bs_k, ld_v, bs_v; /* multiples of 8; ld >= kv_heads * D/H; bs >= 0 (0: shared) */
+  int S;                   /* padded key count, >= 1 */
+  int kv_heads;            /* divides H: query head h reads key head h / (H / kv_heads) */
+  const int32_t* kv_len;   /* (device) int32 [B] keys of each sequence, in [0, S]; NULL: S */
+  const uint8_t* kv_mask;  /* (device) uint8 [B, S], 0 = key not seen; NULL: all seen.  S <= 131072 */
+  float scale;             /* of the scores; 0: 1 / sqrt(D/H) */
+  void* o;                 /* (device) bf16 [n, D] out, rows of the sequences only */
+} hsa_cross_args;
+
+/*
+ * o[m] = sum_j softmax_j(scale q[m] . k[b][j]) v[b][j] per head, over the keys
+ * j < kv_len[b] that kv_mask[b] lets through; b is the sequence of row m.  Statistics and sums in
+ * fp32.  A row without any key gets zeros.  What lies in unseen keys and values (NaN,
+ * infinities) never reaches the result.  Rows of no sequence are left as they were.
+ * q_start, kv_len and kv_mask are read on the device, so a captured graph
+ * serves later prompts of other lengths.  A kv_len outside [0, S] is clamped, a q_start
+ * that descends or leaves [0, n] is clamped; both are reported by hsa_sync_check.
+ */
+hsa_status hsa_cross_attention(hsa_ctx* ctx, const hsa_cross_args* a);
+
 /*
  * Group selection without any device allocation.  The paper has no
  * counterpart: this is a service for callers that cannot call cudaMalloc,

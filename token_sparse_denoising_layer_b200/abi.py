@@ -22,7 +22,9 @@ SYMBOLS = [
     "hsa_select_groups", "hsa_ln_gather", "hsa_qkv_project", "hsa_qkv_project_peers", "hsa_linear", "hsa_kv_scatter", "hsa_kv_scatter_packed",
     "hsa_attention", "hsa_attention_kv", "hsa_out_proj_residual", "hsa_mlp_residual",
     "hsa_ln_gather_mod", "hsa_out_proj_residual_gated", "hsa_mlp_residual_mod",
-    "hsa_layer_forward", "hsa_layer_forward_cond", "hsa_embed", "hsa_head", "hsa_euler_step", "hsa_euler_step_score", "hsa_step", "hsa_step_cond",
+    "hsa_layer_forward", "hsa_layer_forward_cond", "hsa_quant_rows", "hsa_linear_quant",
+    "hsa_ln_gather_quant", "hsa_rope_table", "hsa_rope", "hsa_qk_norm_rope", "hsa_cross_attention",
+    "hsa_embed", "hsa_head", "hsa_euler_step", "hsa_euler_step_score", "hsa_step", "hsa_step_cond",
     "hsa_select_groups_static",
 ]
 
@@ -56,6 +58,33 @@ class hsa_cross_attn(ctypes.Structure):
 
 class hsa_cond(ctypes.Structure):
     _fields_ = [("mod", ctypes.POINTER(ctypes.c_void_p)), ("xa", ctypes.POINTER(hsa_cross_attn))]
+
+
+class hsa_rope_cfg(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int), ("dims", ctypes.c_int * 3), ("base", ctypes.c_double),
+                ("scaling", ctypes.c_int), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("fast", ctypes.c_double),
+                ("slow", ctypes.c_double), ("amp", ctypes.c_double)]
+
+
+class hsa_qk_rope(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int), ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("table", ctypes.c_void_p), ("P", ctypes.c_int),
+                ("rot", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class hsa_cross_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("n", ctypes.c_int),
+                ("B", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("ld_k", ctypes.c_int64), ("bs_k", ctypes.c_int64), ("ld_v", ctypes.c_int64),
+                ("bs_v", ctypes.c_int64), ("S", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("kv_len", ctypes.c_void_p), ("kv_mask", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("o", ctypes.c_void_p)]
+
+
+ROPE_LAYOUT = {"interleaved": 0, "half": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+QK_NORM = {"none": 0, "head": 1, "row": 2}
 
 
 class hsa_model_weights(ctypes.Structure):
@@ -92,6 +121,7 @@ def load() -> ctypes.CDLL:
                            "`python -m token_sparse_denoising_layer_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    L = ctypes.c_int64
     sig = {
         "hsa_create": (I, [ctypes.POINTER(hsa_model_cfg), I, ctypes.POINTER(I), ctypes.POINTER(I),
                            I, I, P, ctypes.POINTER(P)]),
@@ -124,6 +154,14 @@ def load() -> ctypes.CDLL:
         "hsa_layer_forward": (I, [P, ctypes.POINTER(hsa_layer_weights), P, P, I, P, P]),
         "hsa_layer_forward_cond": (I, [P, ctypes.POINTER(hsa_layer_weights), P,
                                        ctypes.POINTER(hsa_cross_attn), P, P, I, P, P]),
+        "hsa_quant_rows": (I, [P, P, I, I, I, L, P, L, P]),
+        "hsa_linear_quant": (I, [P, P, L, P, I, I, P, L, P, I, P]),
+        "hsa_ln_gather_quant": (I, [P, P, P, I, P, P, P, P]),
+        "hsa_rope_table": (I, [P, ctypes.POINTER(hsa_rope_cfg), P, I, P]),
+        "hsa_rope": (I, [P, P, L, I, I, I, P, I, I, P, I, I, P, L]),
+        "hsa_qk_norm_rope": (I, [P, ctypes.POINTER(hsa_qk_rope), P, P, I, P, L, P, P, L, P, P, L,
+                                 P]),
+        "hsa_cross_attention": (I, [P, ctypes.POINTER(hsa_cross_args)]),
         "hsa_embed": (I, [P, P, P, P, I, P]),
         "hsa_head": (I, [P, P, P, P, I, P]),
         "hsa_euler_step": (I, [P, P, P, P, P, P, F, F]),
@@ -168,9 +206,10 @@ def _check(ctx, status: int) -> None:
 class Context:
     """Owns an ``hsa_ctx*``; the handle is ``.ptr``.  Destroyed with ``close()`` or on GC."""
 
-    def __init__(self, ptr: int, cfg: hsa_model_cfg):
+    def __init__(self, ptr: int, cfg: hsa_model_cfg, device: Optional[int] = None):
         self.ptr = ptr
         self.cfg = cfg
+        self.device = device  # CUDA device that was current at hsa_create
 
     def close(self) -> None:
         if self.ptr:
@@ -201,7 +240,8 @@ def hsa_create(N: int, D: int, H: int, F: int, L: int, T: int, budgets: Sequence
     out = ctypes.c_void_p()
     st = lib.hsa_create(ctypes.byref(cfg), T, b, c, K, m, _stream_ptr(stream), ctypes.byref(out))
     _check(None, st)
-    return Context(out.value, cfg)
+    import torch
+    return Context(out.value, cfg, torch.cuda.current_device())
 
 
 def hsa_destroy(ctx: Context) -> None:
@@ -361,6 +401,174 @@ def hsa_layer_forward_cond(ctx: Context, w: hsa_layer_weights, mod, xa, x, idx, 
         ctx.ptr, ctypes.byref(w), _p(mod) if mod is not None else None,
         ctypes.byref(xa) if xa is not None else None, _p(x), _p(idx), n, _p(k_cache),
         _p(v_cache)))
+
+
+def _choice(table: dict, name: str, what: str) -> int:
+    if name not in table:
+        raise ValueError(f"{what} must be one of {', '.join(table)}, got {name!r}")
+    return table[name]
+
+
+def _on_device(ctx: "Optional[Context]", t, what: str) -> None:
+    if not t.is_cuda:
+        raise ValueError("libhsa takes CUDA tensors")
+    if ctx is not None and ctx.device is not None and t.get_device() != ctx.device:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the context on cuda:{ctx.device}")
+
+
+def _typed(ctx: Optional[Context], t, n: int, dtype: str, what: str) -> Optional[int]:
+    """Device address of a contiguous tensor of at least n elements of a type."""
+    if t is None:
+        return None
+    if str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{what} needs {n} elements, has {t.numel()}")
+    _on_device(ctx, t, what)
+    return _p(t)
+
+
+def _rows(ctx: Context, t, n: int, width: int, dtypes: Sequence[str], what: str):
+    """(address, row distance in elements) of a 2-D tensor with dense rows."""
+    if t is None:
+        return None, 0
+    if str(t.dtype) not in ["torch." + d for d in dtypes]:
+        raise ValueError(f"{what} must be {' or '.join(dtypes)}, got {t.dtype}")
+    _on_device(ctx, t, what)
+    if t.dim() != 2 or t.shape[0] < n or t.shape[1] < width:
+        raise ValueError(f"{what} must be [>= {n}, >= {width}], got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have dense rows")
+    # a single row has no distance to the next: any legal one will do
+    ld = t.stride(0) if t.shape[0] > 1 else (width + 15) // 16 * 16
+    return t.data_ptr(), ld
+
+
+def hsa_quant_rows(ctx: Context, a, n: int, Kd: int, q, scale) -> None:
+    """a [>= n, >= Kd] bf16 or fp32 (rows may be strided) -> q int8 rows, scale fp32 [n]."""
+    pa, lda = _rows(ctx, a, n, Kd, ("bfloat16", "float32"), "a")
+    pq, ldq = _rows(ctx, q, n, Kd, ("int8",), "q")
+    kind = 1 if str(a.dtype) == "torch.float32" else 0
+    _check(ctx.ptr, load().hsa_quant_rows(ctx.ptr, pa, kind, n, Kd, lda, pq, ldq,
+                                          _typed(ctx, scale, n, "float32", "scale")))
+
+
+def hsa_linear_quant(ctx: Context, a, a_scale, M: int, Kd: int, w, w_scale, Ncols: int,
+                     out) -> None:
+    """out bf16 [M, Ncols] = (a_scale w_scale) a w^T for int8 rows a [M, ..], w [Ncols, ..]
+    whose rows are a multiple of 16 bytes apart."""
+    pa, lda = _rows(ctx, a, M, Kd, ("int8",), "a")
+    pw, ldw = _rows(ctx, w, Ncols, Kd, ("int8",), "w")
+    _check(ctx.ptr, load().hsa_linear_quant(
+        ctx.ptr, pa, lda, _typed(ctx, a_scale, M, "float32", "a_scale"), M, Kd, pw, ldw,
+        _typed(ctx, w_scale, Ncols, "float32", "w_scale"), Ncols,
+        _typed(ctx, out, M * Ncols, "bfloat16", "out")))
+
+
+def hsa_ln_gather_quant(ctx: Context, x, idx, n: int, q, scale, shift=None, mscale=None) -> None:
+    D = ctx.cfg.D
+    _check(ctx.ptr, load().hsa_ln_gather_quant(
+        ctx.ptr, _typed(ctx, x, ctx.cfg.N * D, "float32", "x"), _typed(ctx, idx, n, "int32", "idx"), n,
+        _typed(ctx, q, n * D, "int8", "q"), _typed(ctx, scale, n, "float32", "scale"),
+        _typed(ctx, shift, D, "float32", "shift"), _typed(ctx, mscale, D, "float32", "mscale")))
+
+
+def rope_cfg(dims: Sequence[int], base: float = 10000.0, scaling: str = "none",
+             factor: float = 1.0, orig_len: float = 0.0, fast: float = 32.0, slow: float = 1.0,
+             amp: float = 1.0) -> hsa_rope_cfg:
+    """Rotated places of each position axis and how frequencies are scaled (include/hsa.h)."""
+    if not 1 <= len(dims) <= 3:
+        raise ValueError("a rotary table has 1 to 3 axes")
+    d3 = (ctypes.c_int * 3)(*dims)
+    return hsa_rope_cfg(len(dims), d3, base, _choice(ROPE_SCALING, scaling, "scaling"), factor, orig_len, fast, slow,
+                        amp)
+
+
+def hsa_rope_table(ctx: Context, cfg: hsa_rope_cfg, pos, P: int, table) -> None:
+    """pos int32 [P, n_axes] or None (one axis, positions 0..P-1); table fp32 [P, rot/2, 2]."""
+    rot = sum(cfg.dims[:max(0, min(cfg.n_axes, 3))])
+    _check(ctx.ptr, load().hsa_rope_table(ctx.ptr, ctypes.byref(cfg),
+                                          _typed(ctx, pos, P * cfg.n_axes, "int32", "pos"), P,
+                                          _typed(ctx, table, P * rot, "float32", "table")))
+
+
+def hsa_rope(ctx: Context, x, n: int, heads: int, table, P: int, rot: int, out,
+             layout: str = "half", pos=None, inverse: bool = False) -> None:
+    """Rotate the first ``rot`` places of each of ``heads`` heads of n rows; out may be x."""
+    width = heads * (ctx.cfg.D // ctx.cfg.H)
+    px, ldx = _rows(ctx, x, n, width, ("bfloat16", "float32"), "x")
+    po, ldo = _rows(ctx, out, n, width, (str(x.dtype)[6:],), "out")
+    kind = 1 if str(x.dtype) == "torch.float32" else 0
+    _check(ctx.ptr, load().hsa_rope(ctx.ptr, px, ldx, kind, n, heads,
+                                    _typed(ctx, table, P * rot, "float32", "table"), P, rot,
+                                    _typed(ctx, pos, n, "int32", "pos"), _choice(ROPE_LAYOUT, layout, "layout"),
+                                    1 if inverse else 0, po, ldo))
+
+
+def qk_rope(norm: str = "head", w_q=None, w_k=None, eps: float = 1e-6, table=None, P: int = 0,
+            rot: int = 0, layout: str = "half") -> hsa_qk_rope:
+    """The struct holds raw device addresses, so it also keeps the tensors alive."""
+    s = hsa_qk_rope(_choice(QK_NORM, norm, "norm"), _typed(None, w_q, 1, "float32", "w_q"),
+                    _typed(None, w_k, 1, "float32", "w_k"), eps,
+                    _typed(None, table, P * rot, "float32", "table"), P, rot, _choice(ROPE_LAYOUT, layout, "layout"))
+    s._keep = (w_q, w_k, table)
+    return s
+
+
+def hsa_qk_norm_rope(ctx: Context, a: hsa_qk_rope, idx, n: int, q, k_cache=None, v_cache=None,
+                     q_in=None, k_in=None, v_in=None, pos=None) -> None:
+    """Norm and rotation of n fresh query and key rows, and the cache write
+    (include/hsa.h).  q_in / k_in / v_in may be strided rows, e.g. column
+    blocks of a packed [n, 3 D] product; without q_in (k_in) the queries (the
+    cache rows idx) change in place."""
+    D, N = ctx.cfg.D, ctx.cfg.N
+    w_q, w_k, table = getattr(a, "_keep", (None, None, None))
+    width = 0 if a.norm == 0 else D if a.norm == 2 else D // ctx.cfg.H
+    _typed(ctx, w_q, width, "float32", "w_q")
+    _typed(ctx, w_k, width, "float32", "w_k")
+    _typed(ctx, table, 0, "float32", "table")
+    pq, ldq = _rows(ctx, q_in, n, D, ("bfloat16",), "q_in")
+    pk, ldk = _rows(ctx, k_in, n, D, ("bfloat16",), "k_in")
+    pv, ldv = _rows(ctx, v_in, n, D, ("bfloat16",), "v_in")
+    _check(ctx.ptr, load().hsa_qk_norm_rope(
+        ctx.ptr, ctypes.byref(a), _typed(ctx, idx, n, "int32", "idx"), _typed(ctx, pos, n, "int32", "pos"),
+        n, pq, ldq, _typed(ctx, q, n * D, "bfloat16", "q"), pk, ldk,
+        _typed(ctx, k_cache, N * D, "bfloat16", "k_cache"), pv, ldv,
+        _typed(ctx, v_cache, N * D, "bfloat16", "v_cache")))
+
+
+def _padded(ctx: Context, t, B: int, S: int, width: int, what: str):
+    """(address, row distance, sequence distance) of encoder states [B, S, width]."""
+    if str(t.dtype) != "torch.bfloat16":
+        raise ValueError(f"{what} must be bfloat16, got {t.dtype}")
+    _on_device(ctx, t, what)
+    if t.dim() != 3 or t.shape[0] < B or t.shape[1] < S or t.shape[2] < width:
+        raise ValueError(f"{what} must be [>= {B}, >= {S}, >= {width}], got {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{what} must have dense rows")
+    ld = t.stride(1) if t.shape[1] > 1 else width
+    return t.data_ptr(), ld, t.stride(0) if t.shape[0] > 1 else ld * S
+
+
+def hsa_cross_attention(ctx: Context, q, q_start, n: int, B: int, k, v, S: int, o, kv_len=None,
+                        kv_mask=None, kv_heads: Optional[int] = None, scale: float = 0.0) -> None:
+    """q, o bf16 [n, D]; q_start int32 [B + 1]; k, v bf16 [B, S, kv_heads * D/H] (rows and
+    sequences may be strided, a sequence distance of 0 shares one); kv_len int32 [B];
+    kv_mask uint8 or bool [B, S], non-zero = seen (include/hsa.h)."""
+    D, H = ctx.cfg.D, ctx.cfg.H
+    kvh = H if kv_heads is None else kv_heads
+    width = kvh * (D // H)
+    pk, ldk, bsk = _padded(ctx, k, B, S, width, "k")
+    pv, ldv, bsv = _padded(ctx, v, B, S, width, "v")
+    if kv_mask is not None and str(kv_mask.dtype) == "torch.bool":
+        import torch
+        kv_mask = kv_mask.view(torch.uint8)
+    args = hsa_cross_args(_typed(ctx, q, n * D, "bfloat16", "q"),
+                          _typed(ctx, q_start, B + 1, "int32", "q_start"), n, B, pk, pv, ldk, bsk, ldv,
+                          bsv, S, kvh, _typed(ctx, kv_len, B, "int32", "kv_len"),
+                          _typed(ctx, kv_mask, B * S, "uint8", "kv_mask"), scale,
+                          _typed(ctx, o, n * D, "bfloat16", "o"))
+    _check(ctx.ptr, load().hsa_cross_attention(ctx.ptr, ctypes.byref(args)))
 
 
 def hsa_embed(ctx: Context, w_in, x_lat, idx, n: int, h) -> None:

@@ -6,6 +6,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
 
@@ -94,6 +95,51 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
   const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    if (why) *why = "cuTensorMapEncodeTiled failed (code " + std::to_string(static_cast<int>(r)) + ")";
+    return false;
+  }
+  return true;
+}
+
+bool make_tmap_s8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
+                  uint32_t box_rows, std::string* why) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) {
+    if (why) *why = "cuTensorMapEncodeTiled is not available from the driver";
+    return false;
+  }
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {ld};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    if (why) *why = "cuTensorMapEncodeTiled failed (code " + std::to_string(static_cast<int>(r)) + ")";
+    return false;
+  }
+  return true;
+}
+
+bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t depth, uint64_t rows,
+                       uint64_t cols, uint64_t row_stride, uint64_t depth_stride,
+                       uint32_t box_rows, std::string* why) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) {
+    if (why) *why = "cuTensorMapEncodeTiled is not available from the driver";
+    return false;
+  }
+  const cuuint64_t dims[3] = {cols, rows, depth};
+  const cuuint64_t strides[2] = {row_stride * 2, depth_stride * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -656,6 +702,240 @@ hsa_status hsa_layer_forward_cond(hsa_ctx* ctx, const hsa_layer_weights* w, cons
     st = mlp_residual(ctx, w->w_1, w->w_2, x, idx, n, row(3), row(4), row(5));
   }
   return st;
+}
+
+namespace {
+
+// NULL or 16-byte aligned.
+bool aligned16_or_null(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+hsa_status check_rope(hsa_ctx* ctx, const float* table, int P, int rot, int layout) {
+  const int hd = ctx->c.cfg.D / ctx->c.cfg.H;
+  HSA_CHECK_PTR(ctx, table);
+  if (P < 1) return fail(ctx, HSA_ERR_INVALID_ARG, "a rotary table needs P >= 1 rows");
+  if (rot < 16 || rot > hd || rot % 16 != 0)
+    return fail(ctx, HSA_ERR_SHAPE, "rot must be a multiple of 16 in [16, D/H], got " + std::to_string(rot));
+  if (layout != HSA_ROPE_INTERLEAVED && layout != HSA_ROPE_HALF)
+    return fail(ctx, HSA_ERR_INVALID_ARG, "unknown rotary layout");
+  return HSA_OK;
+}
+
+}  // namespace
+
+hsa_status hsa_quant_rows(hsa_ctx* ctx, const void* a, int a_type, int n, int Kd, int64_t ld_a,
+                          int8_t* q, int64_t ld_q, float* scale) {
+  HSA_CHECK_CTX(ctx);
+  if (a_type != HSA_BF16 && a_type != HSA_F32)
+    return fail(ctx, HSA_ERR_INVALID_ARG, "quant_rows takes HSA_BF16 or HSA_F32 rows");
+  if (n < 0 || Kd < 1 || Kd > hsa::kMaxQuantK)
+    return fail(ctx, HSA_ERR_SHAPE, "quant_rows needs n >= 0 and 1 <= Kd <= 131071");
+  if (ld_a < Kd || ld_q < Kd || ld_q % 16 != 0)
+    return fail(ctx, HSA_ERR_SHAPE, "quant_rows needs ld_a >= Kd and ld_q >= Kd, a multiple of 16");
+  if (n == 0) return HSA_OK;
+  HSA_CHECK_PTR(ctx, a);
+  HSA_CHECK_PTR(ctx, q);
+  HSA_CHECK_PTR(ctx, scale);
+  hsa::DeviceScope dev(ctx->c.device);
+  return launched(ctx, hsa::launch_quant_rows(ctx->c, a, a_type == HSA_F32, n, Kd, ld_a, q, ld_q, scale),
+                  "quant_rows");
+}
+
+hsa_status hsa_linear_quant(hsa_ctx* ctx, const int8_t* a, int64_t ld_a, const float* a_scale,
+                            int M, int Kd, const int8_t* w, int64_t ld_w, const float* w_scale,
+                            int Ncols, void* out) {
+  HSA_CHECK_CTX(ctx);
+  if (M < 0 || Ncols < 1 || Kd < 1 || Kd > hsa::kMaxQuantK)
+    return fail(ctx, HSA_ERR_SHAPE, "linear_quant needs M >= 0, Ncols >= 1 and 1 <= Kd <= 131071");
+  if (ld_a < Kd || ld_w < Kd || ld_a % 16 != 0 || ld_w % 16 != 0)
+    return fail(ctx, HSA_ERR_SHAPE, "linear_quant needs ld_a, ld_w >= Kd, multiples of 16");
+  if (M == 0) return HSA_OK;
+  HSA_CHECK_PTR(ctx, a);
+  HSA_CHECK_PTR(ctx, a_scale);
+  HSA_CHECK_PTR(ctx, w);
+  HSA_CHECK_PTR(ctx, w_scale);
+  HSA_CHECK_PTR(ctx, out);
+  hsa::DeviceScope dev(ctx->c.device);
+  hsa::GemmArgs g{};
+  g.A = a;
+  g.B = w;
+  g.M = M;
+  g.Ncols = Ncols;
+  g.Kd = Kd;
+  g.epi = hsa::EPI_STORE;
+  g.out = out;
+  g.ld_out = Ncols;
+  g.a_scale = a_scale;
+  g.b_scale = w_scale;
+  g.ld_a = ld_a;
+  g.ld_b = ld_w;
+  std::string why;
+  return launched(ctx, hsa::launch_gemm_s8(ctx->c, g, &why), "linear_quant", why);
+}
+
+hsa_status hsa_ln_gather_quant(hsa_ctx* ctx, const float* x, const int32_t* idx, int n, int8_t* q,
+                               float* scale, const float* shift, const float* mscale) {
+  HSA_CHECK_CTX(ctx);
+  if (hsa_status st = check_n(ctx, n)) return st;
+  if (ctx->c.cfg.D > hsa::kMaxLnQuantD)
+    return fail(ctx, HSA_ERR_SHAPE, "ln_gather_quant needs D <= 5120");
+  if ((shift == nullptr) != (mscale == nullptr))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "shift and mscale are given together or not at all");
+  if (!aligned16_or_null(shift) || !aligned16_or_null(mscale))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "modulation rows must be 16-byte aligned");
+  if (n == 0) return HSA_OK;
+  HSA_CHECK_PTR(ctx, x);
+  HSA_CHECK_PTR(ctx, idx);
+  HSA_CHECK_PTR(ctx, q);
+  HSA_CHECK_PTR(ctx, scale);
+  hsa::DeviceScope dev(ctx->c.device);
+  return launched(ctx, hsa::launch_ln_gather_quant(ctx->c, x, idx, n, q, scale, shift, mscale),
+                  "ln_gather_quant");
+}
+
+hsa_status hsa_rope_table(hsa_ctx* ctx, const hsa_rope_cfg* cfg, const int32_t* pos, int P,
+                          float* table) {
+  HSA_CHECK_CTX(ctx);
+  if (cfg == nullptr) return fail(ctx, HSA_ERR_INVALID_ARG, "cfg is NULL");
+  const hsa_rope_cfg c = *cfg;
+  if (c.n_axes < 1 || c.n_axes > 3) return fail(ctx, HSA_ERR_SHAPE, "a rotary table has 1 to 3 axes");
+  int rot = 0;
+  for (int x = 0; x < c.n_axes; ++x) {
+    if (c.dims[x] < 2 || c.dims[x] > 2 * hsa::kMaxRopePairs || c.dims[x] % 2 != 0)
+      return fail(ctx, HSA_ERR_SHAPE, "each axis rotates an even number of places, 2 or more");
+    rot += c.dims[x];
+  }
+  if (rot > 2 * hsa::kMaxRopePairs)
+    return fail(ctx, HSA_ERR_SHAPE, "a rotary table turns at most 128 places of a head");
+  if (!(c.base > 1.0) || !isfinite(c.base) || !isfinite(c.amp))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "a rotary table needs a base above 1 and a finite amp");
+  if (c.scaling < HSA_ROPE_PLAIN || c.scaling > HSA_ROPE_PARTS)
+    return fail(ctx, HSA_ERR_INVALID_ARG, "unknown rotary scaling");
+  if (c.scaling != HSA_ROPE_PLAIN && (!(c.factor >= 1.0) || !isfinite(c.factor)))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "a scaled rotary table needs factor >= 1");
+  if (c.scaling == HSA_ROPE_PARTS &&
+      (!(c.orig_len > 0.0) || !isfinite(c.orig_len) || !(c.slow >= 0.0) || !(c.fast > c.slow) || !isfinite(c.fast)))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "scaling by parts needs orig_len > 0 and fast > slow >= 0");
+  if (pos == nullptr && c.n_axes != 1)
+    return fail(ctx, HSA_ERR_INVALID_ARG, "positions of several axes must be given");
+  if (!aligned16_or_null(pos)) return fail(ctx, HSA_ERR_INVALID_ARG, "pos is not 16-byte aligned");
+  if (P < 0) return fail(ctx, HSA_ERR_INVALID_ARG, "P must be >= 0");
+  if (P == 0) return HSA_OK;
+  HSA_CHECK_PTR(ctx, table);
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  hsa::RopeFreqs f{};
+  f.half = rot / 2;
+  f.n_axes = c.n_axes;
+  f.amp = static_cast<float>(c.amp);
+  for (int x = 0, j = 0; x < c.n_axes; ++x) {
+    const double dim = c.dims[x];
+    const double base = c.scaling == HSA_ROPE_BASE && dim > 2.0
+                            ? c.base * pow(c.factor, dim / (dim - 2.0)) : c.base;
+    for (int i = 0; i < c.dims[x] / 2; ++i, ++j) {
+      double w = pow(base, -2.0 * i / dim);
+      if (c.scaling == HSA_ROPE_LINEAR) w /= c.factor;
+      if (c.scaling == HSA_ROPE_PARTS) {
+        double keep = (c.orig_len * w / kTwoPi - c.slow) / (c.fast - c.slow);
+        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        w = (1.0 - keep) * w / c.factor + keep * w;
+      }
+      f.turns[j] = w / kTwoPi;
+      f.axis[j] = static_cast<uint8_t>(x);
+    }
+  }
+  hsa::DeviceScope dev(ctx->c.device);
+  return launched(ctx, hsa::launch_rope_table(ctx->c, f, pos, P, table), "rope_table");
+}
+
+hsa_status hsa_rope(hsa_ctx* ctx, const void* x, int64_t ld_x, int type, int n, int heads,
+                    const float* table, int P, int rot, const int32_t* pos, int layout,
+                    int inverse, void* out, int64_t ld_out) {
+  HSA_CHECK_CTX(ctx);
+  if (type != HSA_BF16 && type != HSA_F32)
+    return fail(ctx, HSA_ERR_INVALID_ARG, "rope takes HSA_BF16 or HSA_F32 rows");
+  if (n < 0 || heads < 1) return fail(ctx, HSA_ERR_SHAPE, "rope needs n >= 0 and heads >= 1");
+  const int64_t width = static_cast<int64_t>(heads) * (ctx->c.cfg.D / ctx->c.cfg.H);
+  const int64_t vec = type == HSA_F32 ? 4 : 8;
+  if (ld_x < width || ld_out < width || ld_x % vec != 0 || ld_out % vec != 0)
+    return fail(ctx, HSA_ERR_SHAPE, "rope needs rows of heads * D/H elements, a multiple of 16 bytes apart");
+  if (hsa_status st = check_rope(ctx, table, P, rot, layout)) return st;
+  if (!aligned16_or_null(pos)) return fail(ctx, HSA_ERR_INVALID_ARG, "pos is not 16-byte aligned");
+  if (pos == nullptr && n > P)
+    return fail(ctx, HSA_ERR_INVALID_ARG, "rope without pos needs a table row for each of its rows");
+  if (n == 0) return HSA_OK;
+  HSA_CHECK_PTR(ctx, x);
+  HSA_CHECK_PTR(ctx, out);
+  hsa::DeviceScope dev(ctx->c.device);
+  return launched(ctx,
+                  hsa::launch_rope(ctx->c, x, ld_x, type == HSA_F32, n, heads, table, P, rot, pos,
+                                   layout == HSA_ROPE_HALF, inverse != 0, out, ld_out),
+                  "rope");
+}
+
+hsa_status hsa_qk_norm_rope(hsa_ctx* ctx, const hsa_qk_rope* a, const int32_t* idx,
+                            const int32_t* pos, int n, const void* q_in, int64_t ld_q, void* q,
+                            const void* k_in, int64_t ld_k, void* k_cache, const void* v_in,
+                            int64_t ld_v, void* v_cache) {
+  HSA_CHECK_CTX(ctx);
+  if (a == nullptr) return fail(ctx, HSA_ERR_INVALID_ARG, "a is NULL");
+  if (hsa_status st = check_n(ctx, n)) return st;
+  const int D = ctx->c.cfg.D;
+  if (D > hsa::kMaxQkSteps * 512) return fail(ctx, HSA_ERR_SHAPE, "qk_norm_rope needs D <= 10240");
+  if (a->norm < HSA_NORM_NONE || a->norm > HSA_NORM_ROW)
+    return fail(ctx, HSA_ERR_INVALID_ARG, "unknown query/key norm");
+  if (!(a->eps >= 0.f) || !isfinite(a->eps))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (a->table != nullptr)
+    if (hsa_status st = check_rope(ctx, a->table, a->P, a->rot, a->layout)) return st;
+  for (const void* p : {static_cast<const void*>(a->w_q), static_cast<const void*>(a->w_k),
+                        static_cast<const void*>(idx), static_cast<const void*>(pos), q_in,
+                        static_cast<const void*>(q), k_in, static_cast<const void*>(k_cache), v_in,
+                        static_cast<const void*>(v_cache)})
+    if (!aligned16_or_null(p)) return fail(ctx, HSA_ERR_INVALID_ARG, "a pointer is not 16-byte aligned");
+  if ((q_in != nullptr && q == nullptr) || (k_in != nullptr && k_cache == nullptr))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "q_in needs q, k_in needs k_cache");
+  if ((v_in == nullptr) != (v_cache == nullptr))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "v_in and v_cache are given together or not at all");
+  if (q == nullptr && k_cache == nullptr)
+    return fail(ctx, HSA_ERR_INVALID_ARG, "qk_norm_rope needs queries or keys");
+  if ((q_in != nullptr && (ld_q < D || ld_q % 8 != 0)) || (k_in != nullptr && (ld_k < D || ld_k % 8 != 0)) ||
+      (v_in != nullptr && (ld_v < D || ld_v % 8 != 0)))
+    return fail(ctx, HSA_ERR_SHAPE, "ld_q, ld_k and ld_v must be multiples of 8, >= D");
+  if (n == 0) return HSA_OK;
+  hsa::DeviceScope dev(ctx->c.device);
+  const hsa::QkRows r{q_in, k_in, v_in, ld_q, ld_k, ld_v, q, k_cache, v_cache, idx, pos, n};
+  return launched(ctx, hsa::launch_qk_norm_rope(ctx->c, *a, r), "qk_norm_rope");
+}
+
+hsa_status hsa_cross_attention(hsa_ctx* ctx, const hsa_cross_args* a) {
+  HSA_CHECK_CTX(ctx);
+  if (a == nullptr) return fail(ctx, HSA_ERR_INVALID_ARG, "a is NULL");
+  const int H = ctx->c.cfg.H, hd = ctx->c.cfg.D / H;
+  if (a->n < 0 || a->B < 1 || a->S < 1)
+    return fail(ctx, HSA_ERR_SHAPE, "cross_attention needs n >= 0, B >= 1 and S >= 1");
+  if (a->kv_heads < 1 || H % a->kv_heads != 0)
+    return fail(ctx, HSA_ERR_SHAPE, "kv_heads must divide H");
+  const int64_t width = static_cast<int64_t>(a->kv_heads) * hd;
+  for (int64_t ld : {a->ld_k, a->ld_v})
+    if (ld < width || ld % 8 != 0 || ld >= (1ll << 38))
+      return fail(ctx, HSA_ERR_SHAPE, "ld_k and ld_v must be multiples of 8, >= kv_heads * D/H");
+  for (int64_t bs : {a->bs_k, a->bs_v})
+    if (bs < 0 || bs % 8 != 0 || bs >= (1ll << 38))
+      return fail(ctx, HSA_ERR_SHAPE, "bs_k and bs_v must be multiples of 8, >= 0");
+  if (a->kv_mask != nullptr && a->S > hsa::kMaxMaskedKeys)
+    return fail(ctx, HSA_ERR_SHAPE, "a key mask takes S <= 131072");
+  if (!(a->scale >= 0.f) || !isfinite(a->scale))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (a->n == 0) return HSA_OK;
+  HSA_CHECK_PTR(ctx, a->q);
+  HSA_CHECK_PTR(ctx, a->q_start);
+  HSA_CHECK_PTR(ctx, a->k);
+  HSA_CHECK_PTR(ctx, a->v);
+  HSA_CHECK_PTR(ctx, a->o);
+  if (!aligned16_or_null(a->kv_len) || !aligned16_or_null(a->kv_mask))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "kv_len or kv_mask is not 16-byte aligned");
+  hsa::DeviceScope dev(ctx->c.device);
+  std::string why;
+  return launched(ctx, hsa::launch_cross_attention(ctx->c, *a, &why), "cross_attention", why);
 }
 
 hsa_status hsa_embed(hsa_ctx* ctx, const float* w_in, const float* x_lat, const int32_t* idx,

@@ -15,6 +15,12 @@ namespace hsa {
 
 constexpr int kMaxGroups = 8;
 constexpr int kMaxCaches = 8;  // copies of a KV cache one QKV launch can write (ranks of a step)
+constexpr int kMaxRopePairs = 64;  // planes of one head a rotary table can turn (head_dim 128)
+constexpr int kMaxQkSteps = 20;    // 512-place steps of a row the norm + rotation pass holds
+constexpr int kMaxMaskedKeys = 131072;  // keys whose mask bits fit a CTA's shared memory
+// Longest row of an 8-bit product: 128 * 128 * 131071 still fits 32-bit sums.
+constexpr int kMaxQuantK = 131071;
+constexpr int kMaxLnQuantD = 40 * 128;  // widest row of the LayerNorm that quantises
 
 // Bits a kernel can set in the context's device flag (read by hsa_sync_check).
 enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_INDEX = 2, DEV_BAD_SCORE = 4, DEV_BAD_GROUP = 8 };
@@ -118,6 +124,25 @@ cudaError_t ensure_smem_limit(Kernel* kernel, int bytes, int device, std::atomic
   return e;
 }
 
+// Makes the context's device current for a scope, so that a call works from a
+// thread whose current device is another one.
+class DeviceScope {
+ public:
+  explicit DeviceScope(int device) {
+    if (cudaGetDevice(&old_) != cudaSuccess) old_ = device;
+    if (old_ != device) cudaSetDevice(device);
+    else old_ = -1;
+  }
+  ~DeviceScope() {
+    if (old_ >= 0) cudaSetDevice(old_);
+  }
+  DeviceScope(const DeviceScope&) = delete;
+  DeviceScope& operator=(const DeviceScope&) = delete;
+
+ private:
+  int old_ = -1;
+};
+
 // ---- launchers (return cudaGetLastError() of the launch)
 cudaError_t launch_schedule(const Ctx& c, int i, const uint8_t* g, uint8_t* mask, int32_t* idx,
                             int32_t* n_dev);
@@ -169,13 +194,67 @@ struct GemmArgs {
   const float* gate = nullptr;  // EPI_RESID: x[.., j] += gate[j] * C (fp32 [Ncols]) if set
   const int32_t* idx; // EPI_QKV / EPI_RESID
   int N;              // rows of caches / x (bounds for idx)
+  // Signed 8-bit operands when a_scale is set: A [M, Kd] rows ld_a bytes apart,
+  // B [Ncols, Kd] rows ld_b bytes apart, and C scaled by a_scale[m] b_scale[j]
+  // before the epilogue.
+  const float* a_scale = nullptr;
+  const float* b_scale = nullptr;
+  int64_t ld_a = 0, ld_b = 0;
 };
 
 cudaError_t launch_gemm(const Ctx& c, const GemmArgs& a, std::string* why);
+// The same product of signed 8-bit operands with scales (a.a_scale set).
+cudaError_t launch_gemm_s8(const Ctx& c, const GemmArgs& a, std::string* why);
 
 // Attention of n queries against n_kv key/value rows (row stride D).
 cudaError_t launch_attention(const Ctx& c, const void* q, int n, const void* kc, const void* vc,
                              int n_kv, void* o, std::string* why);
+
+// Rotary frequencies as the table kernel takes them.
+struct RopeFreqs {
+  double turns[kMaxRopePairs];  // frequency of each plane / 2 pi
+  uint8_t axis[kMaxRopePairs];  // position axis of each plane
+  int half, n_axes;
+  float amp;
+};
+
+// Rows of the norm + rotation pass: null members are left out (k_in null with
+// k_cache set: the cache rows are normalised and rotated in place).
+struct QkRows {
+  const void *q_in, *k_in, *v_in;
+  int64_t ld_q, ld_k, ld_v;
+  void *q, *k_cache, *v_cache;
+  const int32_t *idx, *pos;
+  int n;
+};
+
+cudaError_t launch_rope_table(const Ctx& c, const RopeFreqs& f, const int32_t* pos, int P,
+                              float* table);
+cudaError_t launch_rope(const Ctx& c, const void* x, int64_t ld_x, bool f32, int n, int heads,
+                        const float* table, int P, int rot, const int32_t* pos, bool half_layout,
+                        bool inverse, void* out, int64_t ld_out);
+cudaError_t launch_qk_norm_rope(const Ctx& c, const hsa_qk_rope& a, const QkRows& r);
+
+// Row quantisation to signed 8 bits (f32: fp32 source, else bf16).
+cudaError_t launch_quant_rows(const Ctx& c, const void* a, bool f32, int n, int Kd, int64_t ld_a,
+                              int8_t* q, int64_t ld_q, float* scale);
+cudaError_t launch_ln_gather_quant(const Ctx& c, const float* x, const int32_t* idx, int n,
+                                   int8_t* q, float* scale, const float* shift,
+                                   const float* mscale);
+
+// Ragged cross-attention (see hsa_cross_attention).
+cudaError_t launch_cross_attention(const Ctx& c, const hsa_cross_args& a, std::string* why);
+
+// TMA descriptor for a row-major matrix of bytes [rows, cols], rows ld bytes
+// apart, with a box of [box_rows, 128] and 128-byte swizzle.
+bool make_tmap_s8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
+                  uint32_t box_rows, std::string* why);
+
+// TMA descriptor for bf16 matrices [depth][rows, cols] with a box of
+// [1][box_rows, 64] and 128-byte swizzle; strides in elements.
+bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t depth, uint64_t rows,
+                       uint64_t cols, uint64_t row_stride, uint64_t depth_stride,
+                       uint32_t box_rows, std::string* why);
 
 // TMA descriptor for a row-major bf16 matrix [rows, cols] with a
 // box of [box_rows, 64] and 128-byte swizzle.  Returns false on failure.

@@ -1,0 +1,564 @@
+// k_cross.cu - cross-attention of ragged sequences of queries to padded
+// sequences of encoder states of another length, on the 5th-generation tensor
+// cores.
+//
+//   o[m] = sum_j softmax_j(scale q[m] . k[b][j]) v[b][j],  b the sequence of
+// row m, over the keys j < kv_len[b] whose mask byte is set.
+//
+// The tile pipeline is that of the active-query attention (k_attn.cu): one CTA
+// works on two 128-query tiles of one head that share every 128-key tile, S
+// and O live in TMEM, P is written over S as bf16 and read from there by the
+// second product, and the two query tiles ping-pong.  What differs:
+//  - Which rows and keys a CTA owns is read on the device.  Units of 256
+//    queries are numbered per head so that sequence b's first unit is
+//    floor(q_start[b] / 256) + b: every sequence has room for its last,
+//    partial unit, the host knows their number (n / 256 + B) without knowing
+//    the lengths, and a CTA finds its sequence by a search over q_start alone.
+//    Units that no row needs return at once.
+//  - Key tiles before the first and after the last seen key are not loaded.
+//    In tiles with unseen keys the scores are replaced by -inf and the unseen
+//    rows of V are zeroed in shared memory before the product reads them: a
+//    weight of 0 would not silence a NaN there.
+//  - Rows without any key get zeros.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "attn_tile.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace hsa {
+
+namespace {
+
+constexpr int kQ = 128;        // queries per tile
+constexpr int kUnitQ = 2 * kQ; // queries per unit
+constexpr int kStages = 2;     // K and V ring depth
+constexpr int kThreads = 320;
+constexpr uint32_t kTmemCols = 512;
+
+template <int HD>
+struct CrossCfg {
+  static constexpr int kRegions = HD / 64;                    // 128-byte column regions
+  static constexpr int kRegionBytes = 128 * 128;
+  static constexpr int kTileBytes = kRegions * kRegionBytes;  // one Q, K or V tile
+  static constexpr int kBitsAt = kTileBytes * (2 + 2 * kStages) + 256;
+  // Every CTA takes all 512 TMEM columns, so only one may be resident per SM.
+  static constexpr int kSmem = HD == 64 ? 160 * 1024 : kBitsAt + 1024 + kMaxMaskedKeys / 8;
+  static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + HD;
+};
+static_assert(CrossCfg<64>::kBitsAt + 1024 + kMaxMaskedKeys / 8 <= CrossCfg<64>::kSmem &&
+                  CrossCfg<128>::kSmem <= 227 * 1024,
+              "cross-attention exceeds the shared memory of a CTA");
+
+struct CrossParams {
+  int n, B, S, group;  // group: query heads per key head
+  bool k_shared, v_shared;  // one key (value) sequence for all (or B = 1)
+  float scale_log2;
+  __nv_bfloat16* o;
+  int ld;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const uint8_t* kv_mask;
+  int* flag;
+  // Work: units [0, n_full) of units_per_head * H whole, the rest split into
+  // `split` key ranges each, merged by k_cross_combine.
+  int units_per_head, n_full, split;
+  float* part_o;
+  float2* part_ml;
+};
+
+__device__ __forceinline__ int clamped(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// Sequence and rows [q0, q1) of unit u of a head, by a 32-way search over the
+// sequences' first units; q0 >= q1: no rows.  Executed by whole warps.
+__device__ __forceinline__ void unit_rows(const CrossParams& p, int u, int& b, int& q0, int& q1) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = p.B;
+  do {
+    const int step = (len + 31) / 32;
+    const int i = lane * step;
+    bool at_or_before = false;
+    if (i < len)
+      at_or_before = clamped(__ldg(p.q_start + lo + i), 0, p.n) / kUnitQ + lo + i <= u;
+    const int c = __popc(__ballot_sync(0xffffffffu, at_or_before));
+    if (c == 0) {  // before the first sequence
+      b = 0, q0 = 1, q1 = 0;
+      return;
+    }
+    const int next = lo + (c - 1) * step;
+    len = min(step, lo + len - next);
+    lo = next;
+  } while (len > 1);
+  b = lo;
+  const int first = clamped(__ldg(p.q_start + b), 0, p.n);
+  const int last = clamped(__ldg(p.q_start + b + 1), 0, p.n);
+  q0 = first + (u - (first / kUnitQ + b)) * kUnitQ;
+  q1 = min(last, q0 + kUnitQ);
+}
+
+// Bits of the keys of tile j that may be seen.
+__device__ __forceinline__ void seen_bits(const uint32_t* bits, int len, int j, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bits != nullptr) {
+      w[i] = bits[4 * j + i];
+    } else {
+      const int left = len - j * kKV - 32 * i;
+      w[i] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+    }
+  }
+}
+
+__device__ __forceinline__ void hide(uint32_t (&sr)[kKV], const uint32_t (&w)[4]) {
+#pragma unroll
+  for (int e = 0; e < kKV; ++e)
+    if (!((w[e >> 5] >> (e & 31)) & 1u)) sr[e] = __float_as_uint(-INFINITY);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CrossParams p) {
+  using Cfg = CrossCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_first, s_last;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;                              // [2] tiles
+  uint8_t* sK = sQ + 2 * Cfg::kTileBytes;          // [kStages]
+  uint8_t* sV = sK + kStages * Cfg::kTileBytes;    // [kStages]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kStages * Cfg::kTileBytes);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = q_full + 1;
+  uint64_t* k_empty = k_full + kStages;
+  uint64_t* v_full = k_empty + kStages;
+  uint64_t* v_empty = v_full + kStages;
+  uint64_t* s_full = v_empty + kStages;  // [2] per query tile
+  uint64_t* p_full = s_full + 2;         // [2]
+  uint64_t* o_done = p_full + 2;         // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
+  uint32_t* s_bits = reinterpret_cast<uint32_t*>(smem + Cfg::kBitsAt);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) {  // one CTA looks the offsets and lengths over
+    for (int i = threadIdx.x; i < p.B; i += kThreads) {
+      const int a = p.q_start[i], e = p.q_start[i + 1];
+      const int len = p.kv_len != nullptr ? p.kv_len[i] : 0;
+      if (a < 0 || e > p.n || a > e || len < 0 || len > p.S) atomicOr(p.flag, DEV_BAD_INDEX);
+    }
+  }
+  int unit, part = -1, piece = 0;
+  if (static_cast<int>(blockIdx.x) < p.n_full) {
+    unit = blockIdx.x;
+  } else {
+    part = blockIdx.x - p.n_full;
+    unit = p.n_full + part / p.split;
+    piece = part % p.split;
+  }
+  const int h = unit / p.units_per_head;
+  int b, q0, q1;
+  unit_rows(p, unit - h * p.units_per_head, b, q0, q1);
+  if (q0 >= q1) return;
+  const int len = p.kv_len != nullptr ? clamped(__ldg(p.kv_len + b), 0, p.S) : p.S;
+  const int col0 = h * HD, kcol0 = h / p.group * HD;
+  const int ntile = q0 + kQ < q1 ? 2 : 1;
+
+  if (threadIdx.x == 0) {
+    s_first = 0x7fffffff;
+    s_last = -1;
+    mbar_init(q_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);  // one arrival per softmax warp
+      mbar_init(&o_done[t], 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  // Key tiles [j0, j0 + nkv) of this CTA: from the first to the last seen key,
+  // or this part's share of them.
+  int lo_tile = 0, hi_tile = (len + kKV - 1) / kKV;
+  const uint32_t* bits = nullptr;
+  if (p.kv_mask != nullptr) {
+    const uint8_t* row = p.kv_mask + static_cast<int64_t>(b) * p.S;
+    for (int w = warp; w < 4 * hi_tile; w += kThreads / 32) {
+      const int key = 32 * w + lane;
+      const bool see = key < len && __ldg(row + key) != 0;
+      const uint32_t word = __ballot_sync(0xffffffffu, see);
+      if (lane == 0) {
+        s_bits[w] = word;
+        if (word != 0u) {
+          atomicMin(&s_first, w);
+          atomicMax(&s_last, w);
+        }
+      }
+    }
+    __syncthreads();
+    bits = s_bits;
+    lo_tile = s_last < 0 ? 0 : s_first / 4;
+    hi_tile = s_last < 0 ? 0 : s_last / 4 + 1;
+  }
+  int j0 = lo_tile, nkv = hi_tile - lo_tile;
+  if (part >= 0) {
+    const int all = nkv;
+    j0 = lo_tile + piece * all / p.split;
+    nkv = lo_tile + (piece + 1) * all / p.split - j0;
+  }
+
+  if (nkv == 0) {
+    // no key in this range: zeros, or an empty part
+    for (int i = threadIdx.x; i < (q1 - q0) * (HD / 8); i += kThreads) {
+      const int r = i / (HD / 8), e = i % (HD / 8);
+      if (part < 0)
+        *reinterpret_cast<uint4*>(p.o + static_cast<size_t>(q0 + r) * p.ld + col0 + 8 * e) =
+            make_uint4(0u, 0u, 0u, 0u);
+      else if (e == 0)
+        p.part_ml[static_cast<size_t>(part) * kUnitQ + r] = make_float2(-FLT_MAX, 0.f);
+    }
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint64_t keep = l2_policy_evict_last();  // a sequence's K/V is shared by its units
+      const int bk = p.k_shared ? 0 : b, bv = p.v_shared ? 0 : b;
+      mbar_arrive_expect_tx(q_full, ntile * Cfg::kTileBytes);
+      for (int t = 0; t < ntile; ++t)
+        for (int r = 0; r < Cfg::kRegions; ++r)
+          tma_load_2d(sQ + t * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmQ, q_full,
+                      col0 + 64 * r, q0 + t * kQ);
+      int j = 0;
+      for (; j < nkv; ++j) {
+        const int s = j % kStages;
+        const uint32_t ph = ((j / kStages) & 1) ^ 1;
+        if (!mbar_wait(&k_empty[s], ph)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&k_full[s], Cfg::kTileBytes);
+        for (int r = 0; r < Cfg::kRegions; ++r)
+          tma_load_3d_hint(sK + s * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmK, &k_full[s],
+                           kcol0 + 64 * r, (j0 + j) * kKV, bk, keep);
+        if (!mbar_wait(&v_empty[s], ph)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&v_full[s], Cfg::kTileBytes);
+        for (int r = 0; r < Cfg::kRegions; ++r)
+          tma_load_3d_hint(sV + s * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmV, &v_full[s],
+                           kcol0 + 64 * r, (j0 + j) * kKV, bv, keep);
+      }
+      if (!ok) {  // let copies already in flight land before the CTA exits
+        (void)mbar_wait(q_full, 0);
+        for (int k = j > kStages ? j - kStages : 0; k < j; ++k) {
+          (void)mbar_wait(&k_full[k % kStages], (k / kStages) & 1);
+          (void)mbar_wait(&v_full[k % kStages], (k / kStages) & 1);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(kQ, kKV, false, false);
+      constexpr uint32_t idPV = idesc_bf16(kQ, HD, false, true);
+      auto issue_s = [&](int t, int s) {
+        const uint32_t q_addr = smem_u32(sQ + t * Cfg::kTileBytes);
+        const uint32_t k_addr = smem_u32(sK + s * Cfg::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * Cfg::kRegionBytes + (kk & 3) * 32;
+          umma_bf16(tmem + (t == 0 ? Cfg::kColS0 : Cfg::kColS1), sdesc_sw128(q_addr + off, 16, 1024),
+                    sdesc_sw128(k_addr + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int t, int s, bool acc) {
+        const uint32_t v_addr = smem_u32(sV + s * Cfg::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kKV / 16; ++kk)
+          umma_bf16_ta(tmem + (t == 0 ? Cfg::kColO0 : Cfg::kColO1),
+                       tmem + (t == 0 ? Cfg::kColS0 : Cfg::kColS1) + kk * 8,
+                       sdesc_sw128(v_addr + kk * 2048, Cfg::kRegionBytes, 1024), idPV,
+                       (acc || kk > 0) ? 1u : 0u);
+      };
+      ok = mbar_wait(q_full, 0) && mbar_wait(&k_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < ntile; ++t) {
+          issue_s(t, 0);
+          umma_commit(&s_full[t]);
+        }
+        umma_commit(&k_empty[0]);
+      }
+      for (int j = 0; j < nkv && ok; ++j) {
+        const int s = j % kStages;
+        const int s1 = (j + 1) % kStages;
+        for (int t = 0; t < ntile && ok; ++t) {
+          // p_full[0] also says that the unseen rows of this V tile are zeroed
+          if (!mbar_wait(&p_full[t], j & 1)) {
+            ok = false;
+            break;
+          }
+          if (t == 0 && !mbar_wait(&v_full[s], (j / kStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          issue_pv(t, s, j > 0);
+          if (t == ntile - 1) umma_commit(&v_empty[s]);
+          if (j + 1 < nkv) {
+            if (t == 0 && !mbar_wait(&k_full[s1], ((j + 1) / kStages) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_s(t, s1);
+            umma_commit(&s_full[t]);
+            if (t == ntile - 1) umma_commit(&k_empty[s1]);
+          } else {
+            umma_commit(&o_done[t]);
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups
+    const int t = (warp - 2) >> 2;  // query tile of this warpgroup
+    const int qd = warp & 3;        // TMEM lane quarter
+    const int row = 32 * qd + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
+    const uint32_t tS = tmem + lane_base + (t == 0 ? Cfg::kColS0 : Cfg::kColS1);
+    const uint32_t tO = tmem + lane_base + (t == 0 ? Cfg::kColO0 : Cfg::kColO1);
+    const bool active = t < ntile;
+    float m_run = -FLT_MAX, l_run = 0.f;
+    for (int j = 0; j < nkv && active; ++j) {
+      uint32_t see[4];
+      seen_bits(bits, len, j0 + j, see);
+      const bool whole = (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu;  // same for all rows
+      if (!whole && t == 0) {
+        // unseen rows of V: whatever they hold must not meet a weight of 0
+        if (!__all_sync(0xffffffffu, mbar_wait(&v_full[j % kStages], (j / kStages) & 1))) {
+          ok = false;
+          break;
+        }
+        if (!((see[qd] >> lane) & 1u)) {
+          uint8_t* vrow = sV + (j % kStages) * Cfg::kTileBytes + row * 128;
+#pragma unroll
+          for (int r = 0; r < Cfg::kRegions; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(vrow + r * Cfg::kRegionBytes + 16 * i) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t sr[kKV];
+      tmem_ld128(tS, sr);
+      if (!whole) hide(sr, see);
+      // As in k_attn.cu: after the first tile the exponentials are taken
+      // against the running max as it stands, and only a row sum past 2^64
+      // (rare) has S read again, the max raised and O and l rescaled.  A row
+      // that has seen no key yet keeps the lowest finite max, so its first
+      // key takes that way too.
+      float m_use = m_run, alpha = 1.0f, rs;
+      if (j == 0) m_use = fmaxf(row_max(sr) * p.scale_log2, -FLT_MAX);
+      uint32_t w[kKV / 2];
+#pragma unroll 1
+      for (int pass = 0;; ++pass) {
+        rs = exp_row(sr, p.scale_log2, m_use, w);
+        const bool over = !(rs <= kSumLimit);
+        if (j == 0 || pass == 1 || !__any_sync(0xffffffffu, over)) break;
+        tmem_ld128(tS, sr);
+        if (!whole) hide(sr, see);
+        const float tmax = row_max(sr) * p.scale_log2;
+        if (over) {
+          m_use = fmaxf(tmax, m_run);
+          alpha = ex2_approx(m_run - m_use);
+        }
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tO + 32 * c, r);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+          tmem_st32(tO + 32 * c, r);
+        }
+        tmem_ld128(tS, sr);
+        if (!whole) hide(sr, see);
+      }
+      tmem_st64(tS, w);
+      l_run = l_run * alpha + rs;
+      m_run = m_use;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[t]);
+    }
+    // epilogue: O / l -> bf16 rows, or, for a key-range part, the unnormalised
+    // O with its (m, l) for k_cross_combine
+    if (active && ok) {
+      if (__all_sync(0xffffffffu, mbar_wait(&o_done[t], 0))) {
+        tc_fence_after();
+        const float inv = 1.0f / l_run;
+        const int qrow = q0 + t * kQ + row;
+        __nv_bfloat16* orow = p.o + static_cast<size_t>(qrow) * p.ld + col0;
+        const size_t prow = static_cast<size_t>(part) * kUnitQ + t * kQ + row;
+        if (part >= 0 && qrow < q1) p.part_ml[prow] = make_float2(m_run, l_run);
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(tO + 32 * c, r);
+          if (qrow >= q1) continue;
+          if (part >= 0) {
+            float4* d4 = reinterpret_cast<float4*>(p.part_o + prow * HD + 32 * c);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              d4[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                  __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
+          } else {
+            uint4* d4 = reinterpret_cast<uint4*>(orow + 32 * c);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              d4[v] = make_uint4(
+                  pack_bf16(__uint_as_float(r[8 * v]) * inv, __uint_as_float(r[8 * v + 1]) * inv),
+                  pack_bf16(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv),
+                  pack_bf16(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv),
+                  pack_bf16(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv));
+          }
+        }
+      } else {
+        ok = false;
+      }
+    }
+  }
+  if (!ok) atomicOr(p.flag, DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Merge the key-range parts of the split units: one warp per query row,
+// O = sum_i O_i 2^(m_i - M) / sum_i l_i 2^(m_i - M) with M = max_i m_i.  Parts
+// without a key (l = 0) hold no O.
+template <int HD>
+__global__ void __launch_bounds__(256) k_cross_combine(const __grid_constant__ CrossParams p) {
+  const int lane = threadIdx.x & 31;
+  const int rr = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int unit = p.n_full + blockIdx.y;
+  const int h = unit / p.units_per_head;
+  int b, q0, q1;
+  unit_rows(p, unit - h * p.units_per_head, b, q0, q1);
+  if (rr >= q1 - q0) return;
+  const size_t part0 = static_cast<size_t>(blockIdx.y) * p.split;
+  float M = -FLT_MAX;
+  for (int i = 0; i < p.split; ++i) M = fmaxf(M, p.part_ml[(part0 + i) * kUnitQ + rr].x);
+  constexpr int kPer = HD / 32;
+  float acc[kPer];
+#pragma unroll
+  for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+  float L = 0.f;
+  for (int i = 0; i < p.split; ++i) {
+    const size_t prow = (part0 + i) * kUnitQ + rr;
+    const float2 ml = p.part_ml[prow];
+    if (ml.y == 0.f) continue;
+    const float wgt = ex2_approx(ml.x - M);
+    L += ml.y * wgt;
+    const float* po = p.part_o + prow * HD;
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) acc[c] += po[lane + 32 * c] * wgt;
+  }
+  const float inv = L == 0.f ? 0.f : 1.0f / L;
+  __nv_bfloat16* orow = p.o + static_cast<size_t>(q0 + rr) * p.ld + h * HD;
+#pragma unroll
+  for (int c = 0; c < kPer; ++c) orow[lane + 32 * c] = __float2bfloat16_rn(acc[c] * inv);
+}
+
+template <int HD>
+cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
+  const int D = c.cfg.D, H = c.cfg.H;
+  const bool k1 = a.B == 1 || a.bs_k == 0, v1 = a.B == 1 || a.bs_v == 0;
+  const uint64_t width = static_cast<uint64_t>(a.kv_heads) * HD;
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap_bf16(&tq, a.q, a.n, D, D, kQ, why)) return cudaErrorInvalidValue;
+  if (!make_tmap_bf16_3d(&tk, a.k, k1 ? 1 : a.B, a.S, width, a.ld_k, k1 ? a.ld_k * a.S : a.bs_k, kKV, why))
+    return cudaErrorInvalidValue;
+  if (!make_tmap_bf16_3d(&tv, a.v, v1 ? 1 : a.B, a.S, width, a.ld_v, v1 ? a.ld_v * a.S : a.bs_v, kKV, why))
+    return cudaErrorInvalidValue;
+  CrossParams p{};
+  p.n = a.n;
+  p.B = a.B;
+  p.S = a.S;
+  p.group = H / a.kv_heads;
+  p.k_shared = k1;
+  p.v_shared = v1;
+  const double scale = a.scale != 0.f ? a.scale : 1.0 / sqrt(static_cast<double>(HD));
+  p.scale_log2 = static_cast<float>(1.4426950408889634 * scale);
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.ld = D;
+  p.q_start = a.q_start;
+  p.kv_len = a.kv_len;
+  p.kv_mask = a.kv_mask;
+  p.flag = c.flag;
+  constexpr int smem = CrossCfg<HD>::kSmem;
+  static std::atomic<uint64_t> smem_set{0};  // per device
+  {
+    const cudaError_t e = ensure_smem_limit(k_cross<HD>, smem, c.device, smem_set);
+    if (e != cudaSuccess) return e;
+  }
+  p.units_per_head = a.n / kUnitQ + a.B;
+  const int64_t units64 = static_cast<int64_t>(p.units_per_head) * H;
+  if (units64 > 0x3fffffff) {
+    if (why) *why = "too many sequences";
+    return cudaErrorInvalidValue;
+  }
+  const int units = static_cast<int>(units64);
+  p.n_full = units;
+  p.split = 1;
+  p.part_o = c.attn_part_o;
+  p.part_ml = reinterpret_cast<float2*>(c.attn_part_ml);
+  k_cross<HD><<<units, kThreads, smem, c.stream>>>(tq, tk, tv, p);
+  c.launches += 1;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_attention(const Ctx& c, const hsa_cross_args& a, std::string* why) {
+  Timed timed(c, TC_ATTN, 4.0 * a.n * a.S * c.cfg.D);  // every key seen
+  return c.cfg.D / c.cfg.H == 128 ? launch_hd<128>(c, a, why) : launch_hd<64>(c, a, why);
+}
+
+}  // namespace hsa

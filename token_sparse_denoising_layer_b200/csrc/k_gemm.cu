@@ -68,6 +68,8 @@ struct EpiParams {
   const int32_t* idx;
   int N;
   int* flag;
+  const float* a_scale;  // 8-bit operands: C = a_scale[m] b_scale[j] (integer sum)
+  const float* b_scale;
 };
 
 struct F2 {
@@ -207,10 +209,61 @@ __device__ __forceinline__ void resid_chunk(const EpiParams& p, const uint32_t (
   __syncwarp();  // the stage is reused by the next chunk
 }
 
+// Integer sums of one chunk of a row -> fp32 products: float(sum) * sa * sb[j].
+// The integer sum is exact, so three roundings to 32 bits are all there are
+// before the epilogue's own.  Columns past Ncols are zero.
+__device__ __forceinline__ void dequant_chunk(const EpiParams& p, uint32_t (&r)[32], float sa,
+                                              int col) {
+  if (col + 32 <= p.Ncols) {
+    const float4* s4 = reinterpret_cast<const float4*>(p.b_scale + col);
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const float4 s = __ldg(s4 + v);
+      const F2 a = mul_x2(mul_x2(F2{__int2float_rn(static_cast<int>(r[4 * v])),
+                                    __int2float_rn(static_cast<int>(r[4 * v + 1]))},
+                                 splat(sa)),
+                          F2{s.x, s.y});
+      const F2 b = mul_x2(mul_x2(F2{__int2float_rn(static_cast<int>(r[4 * v + 2])),
+                                    __int2float_rn(static_cast<int>(r[4 * v + 3]))},
+                                 splat(sa)),
+                          F2{s.z, s.w});
+      r[4 * v] = __float_as_uint(a.x);
+      r[4 * v + 1] = __float_as_uint(a.y);
+      r[4 * v + 2] = __float_as_uint(b.x);
+      r[4 * v + 3] = __float_as_uint(b.y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float s = col + e < p.Ncols ? __ldg(p.b_scale + col + e) : 0.f;
+      r[e] = __float_as_uint(__int2float_rn(static_cast<int>(r[e])) * sa * s);
+    }
+  }
+}
+
+// Store a chunk of a bf16 output whose rows are not 16-byte aligned, or that
+// ends inside the chunk: through shared memory, so that one store instruction
+// covers 32 adjacent columns of one row.
+__device__ __forceinline__ void store_ragged(const EpiParams& p, const uint32_t (&r)[32], int m,
+                                             int col, float* stage) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) stage[lane * 32 + ((e + lane) & 31)] = __uint_as_float(r[e]);
+  __syncwarp();
+  const int m0 = m - lane;
+  if (col + lane < p.Ncols) {
+    __nv_bfloat16* dst = p.out + static_cast<size_t>(m0) * p.ld_out + col + lane;
+    const int rows = p.M - m0 < 32 ? p.M - m0 : 32;
+    for (int k = 0; k < rows; ++k, dst += p.ld_out)
+      *dst = __float2bfloat16_rn(stage[k * 32 + ((lane + k) & 31)]);
+  }
+  __syncwarp();  // the stage is reused by the next chunk
+}
+
 // Drain one accumulator tile: this warp's 32 rows (TMEM lanes at tbase),
 // output row m (this lane's), columns n0 .. n0 + kCols - 1.  TMEM loads run
 // one 32-column chunk ahead of the chunk being stored.
-template <int kCols, int kEpi>
+template <bool kS8, int kCols, int kEpi>
 __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, int m, int n0,
                                            float* stage) {
   constexpr int NC = kCols / 32;
@@ -220,6 +273,7 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
     dst_row = __ldg(p.idx + m);
     if (!row_ok(dst_row, p.N, p.flag)) dst_row = -1;
   }
+  const float sa = kS8 && mrow ? __ldg(p.a_scale + m) : 0.f;
   uint32_t ra[32], rb[32];
   __syncwarp();
   tmem_ld32_nowait(tbase, ra);
@@ -234,7 +288,10 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
     }
     const int col = n0 + 32 * c;
     if (col >= p.Ncols) continue;  // uniform over the warp
-    if (kEpi == EPI_RESID) {
+    if (kS8) dequant_chunk(p, cur, sa, col);
+    if (kS8 && kEpi == EPI_STORE && (col + 32 > p.Ncols || (p.ld_out & 7) != 0)) {
+      store_ragged(p, cur, m, col, stage);
+    } else if (kEpi == EPI_RESID) {
       resid_chunk(p, cur, dst_row, col, stage);
     } else if (mrow) {
       if (kEpi == EPI_STORE || kEpi == EPI_GELU) {
@@ -269,19 +326,28 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
   }
 }
 
-template <int kCols>
+template <bool kS8, int kCols>
 __device__ __forceinline__ void drain(const EpiParams& p, uint32_t tbase, int m, int n0,
                                       float* stage) {
   switch (p.epi) {
-    case EPI_STORE: drain_tile<kCols, EPI_STORE>(p, tbase, m, n0, stage); break;
-    case EPI_GELU: drain_tile<kCols, EPI_GELU>(p, tbase, m, n0, stage); break;
-    case EPI_QKV: drain_tile<kCols, EPI_QKV>(p, tbase, m, n0, stage); break;
-    case EPI_RESID: drain_tile<kCols, EPI_RESID>(p, tbase, m, n0, stage); break;
+    case EPI_STORE: drain_tile<kS8, kCols, EPI_STORE>(p, tbase, m, n0, stage); break;
+    case EPI_GELU: drain_tile<kS8, kCols, EPI_GELU>(p, tbase, m, n0, stage); break;
+    case EPI_QKV: drain_tile<kS8, kCols, EPI_QKV>(p, tbase, m, n0, stage); break;
+    case EPI_RESID: drain_tile<kS8, kCols, EPI_RESID>(p, tbase, m, n0, stage); break;
     default: break;
   }
 }
 
-template <int BN>
+// A K-block is 128 bytes of every operand row: 64 bf16 or 128 signed bytes.
+// Either way it is four MMA steps of 32 bytes, so the two operand types share
+// the tiles, the ring and the descriptors; 8-bit rows may end inside the last
+// K-block (TMA fills the rest with zeros).
+template <bool kS8>
+__host__ __device__ constexpr int k_block() {
+  return kS8 ? 2 * kBK : kBK;
+}
+
+template <bool kS8, int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
            EpiParams p, int n_tiles, int total_tiles) {
@@ -300,7 +366,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   float* stage = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + Cfg::kBarBytes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nk = p.Kd / kBK;
+  constexpr int kKB = k_block<kS8>();
+  const int nk = (p.Kd + kKB - 1) / kKB;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -342,8 +409,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
-          tma_load_2d(sA + s * Cfg::kABytes, &tmA, &full[s], kb * kBK, m0);
-          tma_load_2d(sB + s * Cfg::kBBytes, &tmB, &full[s], kb * kBK, n0);
+          tma_load_2d(sA + s * Cfg::kABytes, &tmA, &full[s], kb * kKB, m0);
+          tma_load_2d(sB + s * Cfg::kBBytes, &tmB, &full[s], kb * kKB, n0);
         }
       }
       if (!ok) {  // let copies already in flight land before the CTA exits
@@ -352,7 +419,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(kBM, BN, false, false);
+      constexpr uint32_t idesc =
+          kS8 ? idesc_s8(kBM, BN) : idesc_bf16(kBM, BN, false, false);
       int it = 0, lt = 0;
       for (int t = blockIdx.x; t < total_tiles && ok; t += gridDim.x, ++lt) {
         const int b = lt & 1;
@@ -375,7 +443,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int kk = 0; kk < kBK / 16; ++kk) {
             const uint64_t ad = sdesc_sw128(a0 + kk * 32, 16, 1024);
             const uint64_t bd = sdesc_sw128(b0 + kk * 32, 16, 1024);
-            umma_bf16(acc, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+            if (kS8) umma_s8(acc, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+            else umma_bf16(acc, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
           }
           umma_commit(&empty[s]);
         }
@@ -399,7 +468,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int m = (t / n_tiles) * kBM + row, n0 = (t % n_tiles) * BN + half * (BN / 2);
       const uint32_t tbase =
           tmem + b * BN + half * (BN / 2) + (static_cast<uint32_t>(32 * q) << 16);
-      drain<BN / 2>(p, tbase, m, n0, stage + (warp - 2) * kStageWarpFloats);
+      drain<kS8, BN / 2>(p, tbase, m, n0, stage + (warp - 2) * kStageWarpFloats);
       // the buffer may be refilled once every lane's TMEM reads are done
       tc_fence_before();
       __syncwarp();
@@ -429,6 +498,7 @@ constexpr int kPairBBytes = 128 * kBK * 2;
 constexpr int kPairStageBytes = kPairABytes + kPairBBytes;
 constexpr int kPairSmem = kPairStages * kPairStageBytes + 256 + kEpiStageBytes + 1024;
 
+template <bool kS8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 EpiParams p, int n_tiles, int total_tiles) {
@@ -448,7 +518,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int nk = p.Kd / kBK;
+  constexpr int kKB = k_block<kS8>();
+  const int nk = (p.Kd + kKB - 1) / kKB;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -488,14 +559,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           }
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
           const uint32_t lead = to_leader(smem_u32(&full[s]));
-          tma_load_2d_pair(sA + s * kPairABytes, &tmA, lead, kb * kBK, m0);
-          tma_load_2d_pair(sB + s * kPairBBytes, &tmB, lead, kb * kBK, n0);
+          tma_load_2d_pair(sA + s * kPairABytes, &tmA, lead, kb * kKB, m0);
+          tma_load_2d_pair(sB + s * kPairBBytes, &tmB, lead, kb * kKB, n0);
         }
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16(256, 256, false, false);
+      constexpr uint32_t idesc =
+          kS8 ? idesc_s8(256, 256) : idesc_bf16(256, 256, false, false);
       int it = 0, lt = 0;
       for (int t = pair; t < total_tiles && ok; t += npairs, ++lt) {
         const int b = lt & 1;
@@ -515,9 +587,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           const uint32_t a0 = smem_u32(sA + s * kPairABytes);
           const uint32_t b0 = smem_u32(sB + s * kPairBBytes);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            umma_bf16_pair(acc, sdesc_sw128(a0 + kk * 32, 16, 1024),
-                           sdesc_sw128(b0 + kk * 32, 16, 1024), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            const uint64_t ad = sdesc_sw128(a0 + kk * 32, 16, 1024);
+            const uint64_t bd = sdesc_sw128(b0 + kk * 32, 16, 1024);
+            if (kS8) umma_s8_pair(acc, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+            else umma_bf16_pair(acc, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          }
           umma_commit_pair(&empty[s], 0x3);
         }
         umma_commit_pair(&acc_full[b], 0x3);
@@ -539,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       const int m = (t / n_tiles) * 256 + rank * 128 + row, n0 = (t % n_tiles) * 256 + half * 128;
       const uint32_t tbase = tmem + b * 256 + half * 128 + (static_cast<uint32_t>(32 * q) << 16);
-      drain<128>(p, tbase, m, n0, stage + (warp - 2) * kStageWarpFloats);
+      drain<kS8, 128>(p, tbase, m, n0, stage + (warp - 2) * kStageWarpFloats);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(b == 0 ? lead_empty0 : lead_empty1);
@@ -574,10 +649,7 @@ static_assert(GemmCfg<256>::kSmem <= 227 * 1024 && GemmCfg<192>::kSmem <= 227 * 
                   GemmCfg<128>::kSmem <= 227 * 1024,
               "GEMM tile exceeds the shared memory of a CTA");
 
-cudaError_t launch_pair(const Ctx& c, const GemmArgs& a, std::string* why) {
-  CUtensorMap ta, tb;
-  if (!make_tmap_bf16(&ta, a.A, a.M, a.Kd, a.Kd, 128, why)) return cudaErrorInvalidValue;
-  if (!make_tmap_bf16(&tb, a.B, a.Ncols, a.Kd, a.Kd, 128, why)) return cudaErrorInvalidValue;
+EpiParams epi_params(const Ctx& c, const GemmArgs& a) {
   EpiParams p{};
   p.M = a.M;
   p.Ncols = a.Ncols;
@@ -592,48 +664,55 @@ cudaError_t launch_pair(const Ctx& c, const GemmArgs& a, std::string* why) {
   p.idx = a.idx;
   p.N = a.N;
   p.flag = c.flag;
+  p.a_scale = a.a_scale;
+  p.b_scale = a.b_scale;
+  return p;
+}
+
+// Operand maps with boxes of box_a and box_b rows of one K-block.
+template <bool kS8>
+bool operand_maps(const GemmArgs& a, uint32_t box_a, uint32_t box_b, CUtensorMap* ta,
+                  CUtensorMap* tb, std::string* why) {
+  if (kS8)
+    return make_tmap_s8(ta, a.A, a.M, a.Kd, a.ld_a, box_a, why) &&
+           make_tmap_s8(tb, a.B, a.Ncols, a.Kd, a.ld_b, box_b, why);
+  return make_tmap_bf16(ta, a.A, a.M, a.Kd, a.Kd, box_a, why) &&
+         make_tmap_bf16(tb, a.B, a.Ncols, a.Kd, a.Kd, box_b, why);
+}
+
+template <bool kS8>
+cudaError_t launch_pair(const Ctx& c, const GemmArgs& a, std::string* why) {
+  CUtensorMap ta, tb;
+  if (!operand_maps<kS8>(a, 128, 128, &ta, &tb, why)) return cudaErrorInvalidValue;
+  const EpiParams p = epi_params(c, a);
   static std::atomic<uint64_t> smem_set{0};  // per device
   {
-    const cudaError_t e = ensure_smem_limit(k_gemm_pair, kPairSmem, c.device, smem_set);
+    const cudaError_t e = ensure_smem_limit(k_gemm_pair<kS8>, kPairSmem, c.device, smem_set);
     if (e != cudaSuccess) return e;
   }
   const int n_tiles = (a.Ncols + 255) / 256;
   const int total = n_tiles * ((a.M + 255) / 256);
   const int pairs = total < c.num_sms / 2 ? total : c.num_sms / 2;
-  k_gemm_pair<<<2 * pairs, kGemmThreads, kPairSmem, c.stream>>>(ta, tb, p, n_tiles, total);
+  k_gemm_pair<kS8><<<2 * pairs, kGemmThreads, kPairSmem, c.stream>>>(ta, tb, p, n_tiles, total);
   c.launches += 1;
   return cudaGetLastError();
 }
 
-template <int BN>
+template <bool kS8, int BN>
 cudaError_t launch_bn(const Ctx& c, const GemmArgs& a, std::string* why) {
   CUtensorMap ta, tb;
-  if (!make_tmap_bf16(&ta, a.A, a.M, a.Kd, a.Kd, kBM, why)) return cudaErrorInvalidValue;
-  if (!make_tmap_bf16(&tb, a.B, a.Ncols, a.Kd, a.Kd, BN, why)) return cudaErrorInvalidValue;
-  EpiParams p{};
-  p.M = a.M;
-  p.Ncols = a.Ncols;
-  p.Kd = a.Kd;
-  p.epi = a.epi;
-  p.out = static_cast<__nv_bfloat16*>(a.out);
-  p.ld_out = a.ld_out;
-  set_caches(p, a);
-  p.x = a.x;
-  p.ld_x = a.ld_x;
-  p.gate = a.gate;
-  p.idx = a.idx;
-  p.N = a.N;
-  p.flag = c.flag;
+  if (!operand_maps<kS8>(a, kBM, BN, &ta, &tb, why)) return cudaErrorInvalidValue;
+  const EpiParams p = epi_params(c, a);
   constexpr int smem = GemmCfg<BN>::kSmem;
   static std::atomic<uint64_t> smem_set{0};  // per device
   {
-    const cudaError_t e = ensure_smem_limit(k_gemm<BN>, smem, c.device, smem_set);
+    const cudaError_t e = ensure_smem_limit(k_gemm<kS8, BN>, smem, c.device, smem_set);
     if (e != cudaSuccess) return e;
   }
   const int n_tiles = (a.Ncols + BN - 1) / BN;
   const int total = n_tiles * ((a.M + kBM - 1) / kBM);
   const int grid = total < c.num_sms ? total : c.num_sms;
-  k_gemm<BN><<<grid, kGemmThreads, smem, c.stream>>>(ta, tb, p, n_tiles, total);
+  k_gemm<kS8, BN><<<grid, kGemmThreads, smem, c.stream>>>(ta, tb, p, n_tiles, total);
   c.launches += 1;
   return cudaGetLastError();
 }
@@ -670,10 +749,16 @@ cudaError_t launch_gemm(const Ctx& c, const GemmArgs& a, std::string* why) {
   if (a.Ncols % 256 == 0 && cost(256, 1.0) < best) best = cost(256, 1.0), bn = 256;
   if (a.Ncols % 192 == 0 && cost(192, 1.03) < best) best = cost(192, 1.03), bn = 192;
   if (cost(128, 1.12) < best) best = cost(128, 1.12), bn = 128;
-  if (bn == -1) return launch_pair(c, a, why);
-  if (bn == 256) return launch_bn<256>(c, a, why);
-  if (bn == 192) return launch_bn<192>(c, a, why);
-  return launch_bn<128>(c, a, why);
+  if (bn == -1) return launch_pair<false>(c, a, why);
+  if (bn == 256) return launch_bn<false, 256>(c, a, why);
+  if (bn == 192) return launch_bn<false, 192>(c, a, why);
+  return launch_bn<false, 128>(c, a, why);
+}
+
+cudaError_t launch_gemm_s8(const Ctx& c, const GemmArgs& a, std::string* why) {
+  if (a.M <= 0) return cudaSuccess;
+  Timed timed(c, TC_GEMM, 2.0 * a.M * a.Ncols * a.Kd);
+  return launch_bn<true, 128>(c, a, why);
 }
 
 }  // namespace hsa
