@@ -50,8 +50,8 @@ def test_binding_rejects_before_the_library():
             (lambda: abi.hsa_rope(ctx, i8, 8, 1, f, 8, 128, i8), "x must be"),
             (lambda: abi.hsa_rope_table(ctx, abi.rope_cfg([64]), f, 8, f), "pos must be"),
             (lambda: abi.hsa_rope_table(ctx, abi.rope_cfg([64]), i[:7], 8, f), "needs 8"),
-            (lambda: abi.hsa_qk_norm_rope(ctx, abi.qk_rope(), i, 8, f), "q must be"),
-            (lambda: abi.hsa_qk_norm_rope(ctx, abi.qk_rope(), i, 8, b, i8), "k_cache must be"),
+            (lambda: abi.hsa_qk_norm_rope(ctx, abi.qk_rope(), None, 8, f), "q must be"),
+            (lambda: abi.hsa_qk_norm_rope(ctx, abi.qk_rope(), None, 8, None, i8), "k_cache must be"),
             (lambda: abi.hsa_cross_attention(ctx, b, i, 8, 1, f[None], f[None], 8, b), "k must be"),
             (lambda: abi.rope_cfg([2, 2, 2, 2]), "axes"),
             (lambda: abi.rope_cfg([64], scaling="ntk"), "scaling must be"),

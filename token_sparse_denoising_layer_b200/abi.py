@@ -409,46 +409,60 @@ def _choice(table: dict, name: str, what: str) -> int:
     return table[name]
 
 
+_dtype_names: dict = {}
+
+
+def _dtype(t) -> str:
+    """Name of a tensor's type ("bfloat16"), looked up once per type."""
+    name = _dtype_names.get(t.dtype)
+    if name is None:
+        name = _dtype_names[t.dtype] = str(t.dtype)[len("torch."):]
+    return name
+
+
 def _on_device(ctx: "Optional[Context]", t, what: str) -> None:
-    if not t.is_cuda:
+    where = t.get_device()
+    if where < 0:
         raise ValueError("libhsa takes CUDA tensors")
-    if ctx is not None and ctx.device is not None and t.get_device() != ctx.device:
-        raise ValueError(f"{what} is on cuda:{t.get_device()}, the context on cuda:{ctx.device}")
+    if ctx is not None and ctx.device is not None and where != ctx.device:
+        raise ValueError(f"{what} is on cuda:{where}, the context on cuda:{ctx.device}")
 
 
 def _typed(ctx: Optional[Context], t, n: int, dtype: str, what: str) -> Optional[int]:
     """Device address of a contiguous tensor of at least n elements of a type."""
     if t is None:
         return None
-    if str(t.dtype) != "torch." + dtype:
+    if _dtype(t) != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
     if t.numel() < n:
         raise ValueError(f"{what} needs {n} elements, has {t.numel()}")
     _on_device(ctx, t, what)
-    return _p(t)
+    if not t.is_contiguous():
+        raise ValueError("libhsa takes contiguous tensors")
+    return t.data_ptr()
 
 
 def _rows(ctx: Context, t, n: int, width: int, dtypes: Sequence[str], what: str):
     """(address, row distance in elements) of a 2-D tensor with dense rows."""
     if t is None:
         return None, 0
-    if str(t.dtype) not in ["torch." + d for d in dtypes]:
+    if _dtype(t) not in dtypes:
         raise ValueError(f"{what} must be {' or '.join(dtypes)}, got {t.dtype}")
     _on_device(ctx, t, what)
-    if t.dim() != 2 or t.shape[0] < n or t.shape[1] < width:
-        raise ValueError(f"{what} must be [>= {n}, >= {width}], got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < n or shape[1] < width:
+        raise ValueError(f"{what} must be [>= {n}, >= {width}], got {tuple(shape)}")
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{what} must have dense rows")
     # a single row has no distance to the next: any legal one will do
-    ld = t.stride(0) if t.shape[0] > 1 else (width + 15) // 16 * 16
-    return t.data_ptr(), ld
+    return t.data_ptr(), stride[0] if shape[0] > 1 else (width + 15) // 16 * 16
 
 
 def hsa_quant_rows(ctx: Context, a, n: int, Kd: int, q, scale) -> None:
     """a [>= n, >= Kd] bf16 or fp32 (rows may be strided) -> q int8 rows, scale fp32 [n]."""
     pa, lda = _rows(ctx, a, n, Kd, ("bfloat16", "float32"), "a")
     pq, ldq = _rows(ctx, q, n, Kd, ("int8",), "q")
-    kind = 1 if str(a.dtype) == "torch.float32" else 0
+    kind = 1 if _dtype(a) == "float32" else 0
     _check(ctx.ptr, load().hsa_quant_rows(ctx.ptr, pa, kind, n, Kd, lda, pq, ldq,
                                           _typed(ctx, scale, n, "float32", "scale")))
 
@@ -497,8 +511,8 @@ def hsa_rope(ctx: Context, x, n: int, heads: int, table, P: int, rot: int, out,
     """Rotate the first ``rot`` places of each of ``heads`` heads of n rows; out may be x."""
     width = heads * (ctx.cfg.D // ctx.cfg.H)
     px, ldx = _rows(ctx, x, n, width, ("bfloat16", "float32"), "x")
-    po, ldo = _rows(ctx, out, n, width, (str(x.dtype)[6:],), "out")
-    kind = 1 if str(x.dtype) == "torch.float32" else 0
+    po, ldo = _rows(ctx, out, n, width, (_dtype(x),), "out")
+    kind = 1 if _dtype(x) == "float32" else 0
     _check(ctx.ptr, load().hsa_rope(ctx.ptr, px, ldx, kind, n, heads,
                                     _typed(ctx, table, P * rot, "float32", "table"), P, rot,
                                     _typed(ctx, pos, n, "int32", "pos"), _choice(ROPE_LAYOUT, layout, "layout"),
@@ -539,15 +553,16 @@ def hsa_qk_norm_rope(ctx: Context, a: hsa_qk_rope, idx, n: int, q, k_cache=None,
 
 def _padded(ctx: Context, t, B: int, S: int, width: int, what: str):
     """(address, row distance, sequence distance) of encoder states [B, S, width]."""
-    if str(t.dtype) != "torch.bfloat16":
+    if _dtype(t) != "bfloat16":
         raise ValueError(f"{what} must be bfloat16, got {t.dtype}")
     _on_device(ctx, t, what)
-    if t.dim() != 3 or t.shape[0] < B or t.shape[1] < S or t.shape[2] < width:
-        raise ValueError(f"{what} must be [>= {B}, >= {S}, >= {width}], got {tuple(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] < B or shape[1] < S or shape[2] < width:
+        raise ValueError(f"{what} must be [>= {B}, >= {S}, >= {width}], got {tuple(shape)}")
+    if stride[2] != 1 and shape[2] > 1:
         raise ValueError(f"{what} must have dense rows")
-    ld = t.stride(1) if t.shape[1] > 1 else width
-    return t.data_ptr(), ld, t.stride(0) if t.shape[0] > 1 else ld * S
+    ld = stride[1] if shape[1] > 1 else width
+    return t.data_ptr(), ld, stride[0] if shape[0] > 1 else ld * S
 
 
 def hsa_cross_attention(ctx: Context, q, q_start, n: int, B: int, k, v, S: int, o, kv_len=None,
@@ -560,7 +575,7 @@ def hsa_cross_attention(ctx: Context, q, q_start, n: int, B: int, k, v, S: int, 
     width = kvh * (D // H)
     pk, ldk, bsk = _padded(ctx, k, B, S, width, "k")
     pv, ldv, bsv = _padded(ctx, v, B, S, width, "v")
-    if kv_mask is not None and str(kv_mask.dtype) == "torch.bool":
+    if kv_mask is not None and _dtype(kv_mask) == "bool":
         import torch
         kv_mask = kv_mask.view(torch.uint8)
     args = hsa_cross_args(_typed(ctx, q, n * D, "bfloat16", "q"),

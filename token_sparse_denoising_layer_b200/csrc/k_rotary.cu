@@ -27,6 +27,7 @@ namespace hsa {
 namespace {
 
 constexpr int kRowWarps = 8;  // warps (rows) per CTA
+constexpr int kQkWarps = 4;   // rows are wide in registers: small blocks leave fewer unused
 
 // ------------------------------------------------------------ table
 struct TableParams {
@@ -41,24 +42,26 @@ struct TableParams {
 // table[p][i] = amp (cos, sin)(2 pi pos turns_i).  The angle is held in 64
 // bits, as turns: only its fraction of a turn matters, and that is taken
 // before anything is rounded to 32 bits, so far positions lose nothing (at
-// 2^20 the fraction is good to 2^-34 of a turn).  The fraction's part below 32 bits
-// enters by the first-order term of the addition theorem.  Two 64-bit
-// products and the reduction per entry instead of a 64-bit sine and cosine.
+// 2^20 the fraction is good to 2^-34 of a turn).  The fraction's part below 32
+// bits enters by the first-order term of the addition theorem.  One 64-bit
+// product and the reduction per entry instead of a 64-bit sine and cosine.
+// A thread keeps one plane and walks over rows: block (half, 256 / half).
 __global__ void __launch_bounds__(256) k_rope_table(const __grid_constant__ TableParams p) {
-  const int64_t total = static_cast<int64_t>(p.P) * p.half;
-  for (int64_t t = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; t < total;
-       t += static_cast<int64_t>(gridDim.x) * 256) {
-    const int row = static_cast<int>(t / p.half);
-    const int i = static_cast<int>(t - static_cast<int64_t>(row) * p.half);
+  const int i = threadIdx.x;
+  const double turns = p.turns[i];
+  const int axis = p.axis[i];
+  const int stride = gridDim.x * blockDim.y;
+  for (int row = blockIdx.x * blockDim.y + threadIdx.y; row < p.P; row += stride) {
     const int32_t at =
-        p.pos == nullptr ? row : __ldg(p.pos + static_cast<int64_t>(row) * p.n_axes + p.axis[i]);
-    const double full = static_cast<double>(at) * p.turns[i];
+        p.pos == nullptr ? row : __ldg(p.pos + static_cast<int64_t>(row) * p.n_axes + axis);
+    const double full = static_cast<double>(at) * turns;
     const double frac = full - rint(full);  // [-1/2, 1/2]
     const float hi = static_cast<float>(frac);
     const float lo = static_cast<float>(frac - static_cast<double>(hi)) * 6.283185307179586f;
     float s, c;
     sincospif(2.0f * hi, &s, &c);
-    p.table[t] = make_float2(p.amp * fmaf(-lo, s, c), p.amp * fmaf(lo, c, s));
+    p.table[static_cast<int64_t>(row) * p.half + i] =
+        make_float2(p.amp * fmaf(-lo, s, c), p.amp * fmaf(lo, c, s));
   }
 }
 
@@ -128,20 +131,42 @@ __device__ __forceinline__ void turn(float (&x)[2][8], const float (&cs)[8], con
   }
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
-  unpack8(*reinterpret_cast<const uint4*>(p), f);
-}
 __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(p) = pack8(f);
-}
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
+
+// 8 values as they lie in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 w;
+  __device__ void load(const __nv_bfloat16* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ void store(__nv_bfloat16* p) const { __stcs(reinterpret_cast<uint4*>(p), w); }
+  __device__ void get(float (&f)[8]) const { unpack8(w, f); }
+  __device__ void set(const float (&f)[8]) { w = pack8(f); }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ void store(float* p) const {
+    __stcs(reinterpret_cast<float4*>(p), a);
+    __stcs(reinterpret_cast<float4*>(p) + 1, b);
+  }
+  __device__ void get(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  __device__ void set(const float (&f)[8]) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
 
 // ------------------------------------------------------------ rotation alone
 struct RopeParams {
@@ -155,9 +180,12 @@ struct RopeParams {
   int* flag;
 };
 
+// kBatch steps of 512/d heads are loaded before the first is stored (out may be
+// x, so the compiler cannot move a load over a store): enough bytes in flight
+// to cover the latency of HBM.
 template <typename T, int HD>
 __global__ void __launch_bounds__(32 * kRowWarps) k_rope(RopeParams p) {
-  constexpr int U = HD / 16, HG = 32 / U;
+  constexpr int U = HD / 16, HG = 32 / U, kBatch = sizeof(T) == 2 ? 4 : 2;
   const int lane = threadIdx.x & 31;
   const int m = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   if (m >= p.n) return;
@@ -165,20 +193,37 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_rope(RopeParams p) {
   const int32_t row = p.pos == nullptr ? m : __ldg(p.pos + m);
   if (!row_ok(row, p.P, p.flag)) return;
   const bool turned = 16 * u < p.rot;
-  float cs[8], sn[8];
-  if (turned) load_turns(p.table, row, p.rot, u, p.inverse, cs, sn);
   int a, b;
   unit_places(u, p.rot, p.half_layout, a, b);
   const T* x = static_cast<const T*>(p.x) + m * p.ld_x;
   T* out = static_cast<T*>(p.out) + m * p.ld_out;
-#pragma unroll 4
-  for (int h = h0; h < p.heads; h += HG) {
-    float f[2][8];
-    load8(x + h * HD + a, f[0]);
-    load8(x + h * HD + b, f[1]);
-    if (turned) turn(f, cs, sn, p.half_layout);
-    store8(out + h * HD + a, f[0]);
-    store8(out + h * HD + b, f[1]);
+  float cs[8], sn[8];
+  if (turned) load_turns(p.table, row, p.rot, u, p.inverse, cs, sn);
+  for (int hb = h0; hb < p.heads; hb += HG * kBatch) {
+    Raw8<T> raw[kBatch][2];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = hb + k * HG;
+      if (h < p.heads) {
+        raw[k][0].load(x + h * HD + a);
+        raw[k][1].load(x + h * HD + b);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = hb + k * HG;
+      if (h >= p.heads) break;
+      if (turned) {
+        float f[2][8];
+        raw[k][0].get(f[0]);
+        raw[k][1].get(f[1]);
+        turn(f, cs, sn, p.half_layout);
+        raw[k][0].set(f[0]);
+        raw[k][1].set(f[1]);
+      }
+      raw[k][0].store(out + h * HD + a);
+      raw[k][1].store(out + h * HD + b);
+    }
   }
 }
 
@@ -202,10 +247,10 @@ struct QkParams {
 // summed in 32 bits: over a head by shuffles between the head's lanes, over
 // the row by all lanes.  One rounding to bf16, at the store.
 template <int HD, int NIT>
-__global__ void __launch_bounds__(32 * kRowWarps) k_qk_norm_rope(QkParams p) {
+__global__ void __launch_bounds__(32 * kQkWarps) k_qk_norm_rope(const __grid_constant__ QkParams p) {
   constexpr int U = HD / 16, HG = 32 / U;
   const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kQkWarps + (threadIdx.x >> 5);
   const int m = static_cast<int>(item / p.parts);
   if (m >= p.n) return;
   const int part = p.part[item - static_cast<int64_t>(m) * p.parts];
@@ -242,26 +287,38 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_qk_norm_rope(QkParams p) {
         *reinterpret_cast<uint4*>(dst + e) = make_uint4(0u, 0u, 0u, 0u);
     return;
   }
-  if (part == 2) {
-    for (int e = 8 * lane; e < D; e += 256)
-      *reinterpret_cast<uint4*>(dst + e) = *reinterpret_cast<const uint4*>(src + e);
-    return;
-  }
-  const bool turned = p.table != nullptr && 16 * u < p.rot;
+  const bool turned = p.table != nullptr && part != 2 && 16 * u < p.rot;
   int a, b;
-  unit_places(u, p.table != nullptr ? p.rot : 0, p.half_layout, a, b);
-  uint4 raw[NIT][2];
+  unit_places(u, p.table != nullptr && part != 2 ? p.rot : 0, p.half_layout, a, b);
+  Raw8<__nv_bfloat16> raw[NIT][2];
 #pragma unroll
   for (int it = 0; it < NIT; ++it) {
     const int h = h0 + it * HG;
-    raw[it][0] = raw[it][1] = make_uint4(0u, 0u, 0u, 0u);
+    raw[it][0].w = raw[it][1].w = make_uint4(0u, 0u, 0u, 0u);
     if (h < p.H) {
-      raw[it][0] = *reinterpret_cast<const uint4*>(src + h * HD + a);
-      raw[it][1] = *reinterpret_cast<const uint4*>(src + h * HD + b);
+      raw[it][0].load(src + h * HD + a);
+      raw[it][1].load(src + h * HD + b);
     }
+  }
+  if (part == 2) {  // values go to the cache as they are
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      const int h = h0 + it * HG;
+      if (h < p.H) {
+        raw[it][0].store(dst + h * HD + a);
+        raw[it][1].store(dst + h * HD + b);
+      }
+    }
+    return;
   }
   float cs[8], sn[8];
   if (turned) load_turns(p.table, at, p.rot, u, false, cs, sn);
+  float g[2][8];  // weights of a norm over each head: the same for all heads
+  const bool per_head = p.norm == HSA_NORM_HEAD, weighted = w != nullptr && p.norm != HSA_NORM_NONE;
+  if (weighted && per_head) {
+    load8(w + a, g[0]);
+    load8(w + b, g[1]);
+  }
   float row_scale = 1.0f;
   if (p.norm == HSA_NORM_ROW) {
     float ss = 0.f;
@@ -270,49 +327,48 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_qk_norm_rope(QkParams p) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float f[8];
-        unpack8(raw[it][k], f);
+        raw[it][k].get(f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
       }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    row_scale = 1.0f / sqrtf(ss / static_cast<float>(D) + p.eps);
+    row_scale = rsqrtf(ss / static_cast<float>(D) + p.eps);
   }
 #pragma unroll
   for (int it = 0; it < NIT; ++it) {
     const int h = h0 + it * HG;
     float f[2][8];
-    unpack8(raw[it][0], f[0]);
-    unpack8(raw[it][1], f[1]);
+    raw[it][0].get(f[0]);
+    raw[it][1].get(f[1]);
     if (p.norm != HSA_NORM_NONE) {
       float scale = row_scale;
-      if (p.norm == HSA_NORM_HEAD) {
+      if (per_head) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(f[0][i], f[0][i], fmaf(f[1][i], f[1][i], ss));
 #pragma unroll
         for (int o = U / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        scale = 1.0f / sqrtf(ss / static_cast<float>(HD) + p.eps);
+        scale = rsqrtf(ss * (1.0f / HD) + p.eps);
       }
-      if (w != nullptr && h < p.H) {
-        const float* wr = w + (p.norm == HSA_NORM_ROW ? h * HD : 0);
-        float g[2][8];
-        load8(wr + a, g[0]);
-        load8(wr + b, g[1]);
+      if (weighted && !per_head && h < p.H) {
+        load8(w + h * HD + a, g[0]);
+        load8(w + h * HD + b, g[1]);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          f[0][i] = f[0][i] * scale * g[0][i];
-          f[1][i] = f[1][i] * scale * g[1][i];
+          f[k][i] *= scale;
+          if (weighted) f[k][i] *= g[k][i];
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[0][i] *= scale, f[1][i] *= scale;
-      }
     }
     if (turned) turn(f, cs, sn, p.half_layout);
+    raw[it][0].set(f[0]);
+    raw[it][1].set(f[1]);
     if (h < p.H) {
-      store8(dst + h * HD + a, f[0]);
-      store8(dst + h * HD + b, f[1]);
+      raw[it][0].store(dst + h * HD + a);
+      raw[it][1].store(dst + h * HD + b);
     }
   }
 }
@@ -322,8 +378,8 @@ cudaError_t launch_qk(const Ctx& c, const QkParams& p) {
   constexpr int HG = 512 / HD;
   const int nit = (p.H + HG - 1) / HG;
   const int64_t items = static_cast<int64_t>(p.n) * p.parts;
-  const unsigned grid = static_cast<unsigned>((items + kRowWarps - 1) / kRowWarps);
-  const dim3 block(32 * kRowWarps);
+  const unsigned grid = static_cast<unsigned>((items + kQkWarps - 1) / kQkWarps);
+  const dim3 block(32 * kQkWarps);
   if (nit <= 1) k_qk_norm_rope<HD, 1><<<grid, block, 0, c.stream>>>(p);
   else if (nit <= 3) k_qk_norm_rope<HD, 3><<<grid, block, 0, c.stream>>>(p);
   else if (nit <= 6) k_qk_norm_rope<HD, 6><<<grid, block, 0, c.stream>>>(p);
@@ -346,9 +402,10 @@ cudaError_t launch_rope_table(const Ctx& c, const RopeFreqs& f, const int32_t* p
   p.half = f.half;
   p.amp = f.amp;
   p.table = reinterpret_cast<float2*>(table);
-  int64_t blocks = (static_cast<int64_t>(P) * f.half + 255) / 256;
-  if (blocks > c.num_sms * 32) blocks = c.num_sms * 32;
-  k_rope_table<<<static_cast<unsigned>(blocks), 256, 0, c.stream>>>(p);
+  const dim3 block(f.half, 256 / f.half);
+  int64_t blocks = (static_cast<int64_t>(P) + block.y - 1) / block.y;
+  if (blocks > c.num_sms * 8) blocks = c.num_sms * 8;
+  k_rope_table<<<static_cast<unsigned>(blocks), block, 0, c.stream>>>(p);
   c.launches += 1;
   return cudaGetLastError();
 }
