@@ -72,33 +72,6 @@ struct EpiParams {
   const float* b_scale;
 };
 
-struct F2 {
-  float x, y;
-};
-
-// d = a * b + c, two lanes per instruction (packed f32x2).
-__device__ __forceinline__ F2 fma_x2(F2 a, F2 b, F2 c) {
-  F2 d;
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-
-__device__ __forceinline__ F2 mul_x2(F2 a, F2 b) {
-  F2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
-__device__ __forceinline__ F2 splat(float v) { return F2{v, v}; }
-
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -241,9 +214,9 @@ __device__ __forceinline__ void dequant_chunk(const EpiParams& p, uint32_t (&r)[
   }
 }
 
-// Store a chunk of a bf16 output whose rows are not 16-byte aligned, or that
-// ends inside the chunk: through shared memory, so that one store instruction
-// covers 32 adjacent columns of one row.
+// Store a chunk of a bf16 output whose rows are not 16-byte aligned: through
+// shared memory, so that one store instruction covers 32 adjacent columns of
+// one row.
 __device__ __forceinline__ void store_ragged(const EpiParams& p, const uint32_t (&r)[32], int m,
                                              int col, float* stage) {
   const int lane = threadIdx.x & 31;
@@ -258,6 +231,38 @@ __device__ __forceinline__ void store_ragged(const EpiParams& p, const uint32_t 
       *dst = __float2bfloat16_rn(stage[k * 32 + ((lane + k) & 31)]);
   }
   __syncwarp();  // the stage is reused by the next chunk
+}
+
+// 32 fp32 values of this lane's row -> bf16 in the warp's stage, columns 32 half ..
+// of a row of 64.  The 16-byte group g of row r lies at group g ^ (r & 7):
+// free of bank conflicts by rows and by columns.
+__device__ __forceinline__ void stage_half(uint8_t* stage, const uint32_t (&r)[32], int half) {
+  const int lane = threadIdx.x & 31;
+  uint4 w[4];
+  pack_bf16x32(r, w);
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    *reinterpret_cast<uint4*>(stage + lane * 128 + 16 * ((4 * half + v) ^ (lane & 7))) = w[v];
+}
+
+// Store the warp's staged rows, up to 64 columns of them from `col` on: one
+// instruction covers four rows and 128 contiguous bytes of each, where a store
+// straight from a lane's own row would touch 32 rows and half a sector of each.
+__device__ __forceinline__ void store_staged(const EpiParams& p, const uint8_t* stage, int m0,
+                                             int col, int end) {
+  const int lane = threadIdx.x & 31;
+  const int g = lane & 7;
+  __syncwarp();
+  if (col + 8 * g < end) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int rr = 4 * k + (lane >> 3);
+      if (m0 + rr < p.M)
+        *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(m0 + rr) * p.ld_out + col + 8 * g) =
+            *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
+    }
+  }
+  __syncwarp();  // the stage is reused by the next 64 columns
 }
 
 // Drain one accumulator tile: this warp's 32 rows (TMEM lanes at tbase),
@@ -289,8 +294,16 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
     const int col = n0 + 32 * c;
     if (col >= p.Ncols) continue;  // uniform over the warp
     if (kS8) dequant_chunk(p, cur, sa, col);
-    if (kS8 && kEpi == EPI_STORE && (col + 32 > p.Ncols || (p.ld_out & 7) != 0)) {
-      store_ragged(p, cur, m, col, stage);
+    if (kS8 && kEpi == EPI_STORE) {
+      if ((p.ld_out & 7) != 0) {
+        store_ragged(p, cur, m, col, stage);
+      } else {
+        uint8_t* bytes = reinterpret_cast<uint8_t*>(stage);
+        stage_half(bytes, cur, c & 1);
+        if ((c & 1) || c + 1 == NC || col + 32 >= p.Ncols)
+          store_staged(p, bytes, m - (threadIdx.x & 31), col - 32 * (c & 1),
+                       min(p.Ncols, col + 32));
+      }
     } else if (kEpi == EPI_RESID) {
       resid_chunk(p, cur, dst_row, col, stage);
     } else if (mrow) {
@@ -758,6 +771,25 @@ cudaError_t launch_gemm(const Ctx& c, const GemmArgs& a, std::string* why) {
 cudaError_t launch_gemm_s8(const Ctx& c, const GemmArgs& a, std::string* why) {
   if (a.M <= 0) return cudaSuccess;
   Timed timed(c, TC_GEMM, 2.0 * a.M * a.Ncols * a.Kd);
+  // As above, by tile-waves x tile width; columns may end inside a tile.
+  const int mt = (a.M + kBM - 1) / kBM;
+  auto cost = [&](int bn, double per_col) {
+    const long tiles = static_cast<long>(mt) * ((a.Ncols + bn - 1) / bn);
+    return static_cast<double>((tiles + c.num_sms - 1) / c.num_sms) * bn * per_col;
+  };
+  double best = 1e300;
+  int bn = 128;
+  if (a.Ncols >= 256 && a.M >= 256) {
+    const long tiles = static_cast<long>((a.M + 255) / 256) * ((a.Ncols + 255) / 256);
+    const int pairs = c.num_sms / 2;
+    best = static_cast<double>((tiles + pairs - 1) / pairs) * 256 * kPairCost, bn = -1;
+  }
+  if (cost(256, 1.0) < best) best = cost(256, 1.0), bn = 256;
+  if (cost(192, 1.03) < best) best = cost(192, 1.03), bn = 192;
+  if (cost(128, 1.12) < best) best = cost(128, 1.12), bn = 128;
+  if (bn == -1) return launch_pair<true>(c, a, why);
+  if (bn == 256) return launch_bn<true, 256>(c, a, why);
+  if (bn == 192) return launch_bn<true, 192>(c, a, why);
   return launch_bn<true, 128>(c, a, why);
 }
 

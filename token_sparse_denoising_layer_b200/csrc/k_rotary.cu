@@ -9,10 +9,10 @@
 // half layout.
 //
 // All three kernels are bound by HBM.  A thread owns a unit of 16 places of a
-// head, eight planes: two 16-byte vectors of bf16, adjacent (interleaved) or
-// rot/2 apart (half), so no plane crosses threads.  A warp owns a row: its 32
-// lanes hold the d/16 units of 512/d heads and step over the heads, keeping
-// the row's 8 cosines and sines per lane in registers for all of them.
+// head, eight planes in two 16-byte vectors of bf16, so no plane crosses
+// threads.  A warp owns a row: its 32 lanes hold the d/16 units of 512/d heads
+// and step over the heads, keeping the row's 8 cosines and sines per lane in
+// registers for all of them.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -31,142 +31,191 @@ constexpr int kQkWarps = 4;   // rows are wide in registers: small blocks leave 
 
 // ------------------------------------------------------------ table
 struct TableParams {
-  double turns[kMaxRopePairs];  // frequency / 2 pi of each plane
+  double quarters[kMaxRopePairs];  // frequency of each plane in quarter turns per position
   uint8_t axis[kMaxRopePairs];
-  const int32_t* pos;           // [P, n_axes], or null: row p has position p
+  const int32_t* pos;              // [P, n_axes], or null: row p has position p
   int n_axes, P, half;
   float amp;
-  float2* table;                // [P, half]
+  float2* table;                   // [P, half]
 };
 
-// table[p][i] = amp (cos, sin)(2 pi pos turns_i).  The angle is held in 64
-// bits, as turns: only its fraction of a turn matters, and that is taken
-// before anything is rounded to 32 bits, so far positions lose nothing (at
-// 2^20 the fraction is good to 2^-34 of a turn).  The fraction's part below 32
-// bits enters by the first-order term of the addition theorem.  One 64-bit
-// product and the reduction per entry instead of a 64-bit sine and cosine.
-// A thread keeps one plane and walks over rows: block (half, 256 / half).
+// table[p][i] = amp (cos, sin)(pos f_i).  The angle is held in 64 bits, as
+// quarter turns: pos * quarters = k + r with k whole and |r| <= 1/2.  Only r
+// and k mod 4 matter, and r is taken before anything is rounded to 32 bits, so
+// far positions lose nothing (at 2^20, r is good to 2^-32 of a turn).  Adding 1.5 * 2^52
+// leaves k in the low bits of the sum, which is exact below 2^51 quarter
+// turns; a 32-bit position and f <= 1 stay below 2^32.  Sine and cosine of
+// x = r pi / 2, |x| <= pi / 4, are their Taylor polynomials to x^9 and x^10
+// (the next terms are below 2e-9), and k mod 4 swaps and negates them.
+// Four 64-bit operations per entry instead of a 64-bit sine and cosine.
+// A thread keeps one plane and walks over rows, the positions of kTableBatch
+// of them loaded together: block (half, 256 / half).
+constexpr int kTableBatch = 4;
+
 __global__ void __launch_bounds__(256) k_rope_table(const __grid_constant__ TableParams p) {
+  constexpr double kRound = 6755399441055744.0;  // 1.5 * 2^52
   const int i = threadIdx.x;
-  const double turns = p.turns[i];
+  const double quarters = p.quarters[i];
   const int axis = p.axis[i];
   const int stride = gridDim.x * blockDim.y;
-  for (int row = blockIdx.x * blockDim.y + threadIdx.y; row < p.P; row += stride) {
-    const int32_t at =
-        p.pos == nullptr ? row : __ldg(p.pos + static_cast<int64_t>(row) * p.n_axes + axis);
-    const double full = static_cast<double>(at) * turns;
-    const double frac = full - rint(full);  // [-1/2, 1/2]
-    const float hi = static_cast<float>(frac);
-    const float lo = static_cast<float>(frac - static_cast<double>(hi)) * 6.283185307179586f;
-    float s, c;
-    sincospif(2.0f * hi, &s, &c);
-    p.table[static_cast<int64_t>(row) * p.half + i] =
-        make_float2(p.amp * fmaf(-lo, s, c), p.amp * fmaf(lo, c, s));
+  for (int64_t row0 = blockIdx.x * blockDim.y + threadIdx.y; row0 < p.P;
+       row0 += kTableBatch * static_cast<int64_t>(stride)) {
+    int32_t at[kTableBatch];
+#pragma unroll
+    for (int n = 0; n < kTableBatch; ++n) {
+      const int64_t row = row0 + n * static_cast<int64_t>(stride);
+      at[n] = row >= p.P ? 0 : p.pos == nullptr ? static_cast<int32_t>(row)
+                                                : __ldg(p.pos + row * p.n_axes + axis);
+    }
+#pragma unroll
+    for (int n = 0; n < kTableBatch; ++n) {
+      const int64_t row = row0 + n * static_cast<int64_t>(stride);
+      if (row >= p.P) break;
+      const double full = static_cast<double>(at[n]) * quarters;
+      const double shifted = full + kRound;
+      const int k = __double2loint(shifted);
+      const float x = static_cast<float>(full - (shifted - kRound)) * 1.5707963267948966f;
+      const float z = x * x;
+      float s = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+      s = fmaf(z, s, 1.f / 120.f);
+      s = fmaf(z, s, -1.f / 6.f);
+      s = fmaf(x * z, s, x);
+      float c = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+      c = fmaf(z, c, -1.f / 720.f);
+      c = fmaf(z, c, 1.f / 24.f);
+      c = fmaf(z, c, -0.5f);
+      c = fmaf(z, c, 1.f);
+      const float u = (k & 1) ? s : c, v = (k & 1) ? c : s;
+      const float cs = ((k + 1) & 2) ? -u : u, sn = (k & 2) ? -v : v;
+      p.table[row * p.half + i] = make_float2(p.amp * cs, p.amp * sn);
+    }
   }
 }
 
 // ------------------------------------------------------------ units of 16 places
-struct Unit {
-  float u[8], v[8];  // plane members in half layout order: (u[i], v[i]) is plane i
+// A lane's unit u of d/16 per head: two vectors of 8 places, at a and b.  In
+// the half layout they are the two members of eight planes; past the rotated
+// places, and in the interleaved layout (where a vector holds whole planes),
+// b lies half of the places in question further on.  Either way a
+// head's lanes cover 16 adjacent bytes each, in two runs.
+template <int HD, bool kHalf>
+struct Places {
+  int a, b;
+  bool turn_a, turn_b;  // whether the vector's places are rotated
+  __device__ Places(int u, int rot) {
+    if (!kHalf) {
+      a = 8 * u, b = HD / 2 + 8 * u;
+      turn_a = a < rot, turn_b = b < rot;
+    } else {
+      turn_a = turn_b = 16 * u < rot;
+      if (turn_a) a = 8 * u, b = rot / 2 + 8 * u;
+      else a = rot + 8 * (u - rot / 16), b = a + (HD - rot) / 2;
+    }
+  }
 };
-
-__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
-  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(r[i] << 16);
-    f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                    pack_bf16(f[6], f[7]));
-}
-
-// The lane's cosines and sines: table row entries 8u .. 8u+7 (64 bytes).
-__device__ __forceinline__ void load_turns(const float* __restrict__ table, int64_t row, int rot,
-                                           int u, bool inverse, float (&cs)[8], float (&sn)[8]) {
-  const float4* t4 = reinterpret_cast<const float4*>(table + row * rot + 16 * u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 w = __ldg(t4 + i);
-    cs[2 * i] = w.x;
-    sn[2 * i] = inverse ? -w.y : w.y;
-    cs[2 * i + 1] = w.z;
-    sn[2 * i + 1] = inverse ? -w.w : w.w;
-  }
-}
-
-// First place (in elements) of the unit's two 8-element vectors within its head.
-__device__ __forceinline__ void unit_places(int u, int rot, bool half_layout, int& a, int& b) {
-  if (half_layout && 16 * u < rot) {
-    a = 8 * u;
-    b = a + rot / 2;
-  } else {
-    a = 16 * u;
-    b = a + 8;
-  }
-}
-
-// Turns a unit's 16 values, x[0] and x[1] its two vectors of 8.
-__device__ __forceinline__ void turn(float (&x)[2][8], const float (&cs)[8], const float (&sn)[8],
-                                     bool half_layout) {
-  if (half_layout) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = x[0][i], b = x[1][i];
-      x[0][i] = a * cs[i] - b * sn[i];
-      x[1][i] = b * cs[i] + a * sn[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float& p = x[i >> 2][2 * (i & 3)];
-      float& q = x[i >> 2][2 * (i & 3) + 1];
-      const float a = p, b = q;
-      p = a * cs[i] - b * sn[i];
-      q = b * cs[i] + a * sn[i];
-    }
-  }
-}
-
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
 
 // 8 values as they lie in memory.
 template <typename T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
-  uint4 w;
-  __device__ void load(const __nv_bfloat16* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ void store(__nv_bfloat16* p) const { __stcs(reinterpret_cast<uint4*>(p), w); }
-  __device__ void get(float (&f)[8]) const { unpack8(w, f); }
-  __device__ void set(const float (&f)[8]) { w = pack8(f); }
+  uint32_t w[4];
+  __device__ void load(const __nv_bfloat16* p) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+  __device__ void store(__nv_bfloat16* p) const {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  __device__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ float get(int i) const {
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+  __device__ void set2(int i, float lo, float hi) { w[i >> 1] = pack_bf16(lo, hi); }
 };
 template <>
 struct Raw8<float> {
-  float4 a, b;
+  float f[8];
   __device__ void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ void store(float* p) const {
-    __stcs(reinterpret_cast<float4*>(p), a);
-    __stcs(reinterpret_cast<float4*>(p) + 1, b);
-  }
-  __device__ void get(float (&f)[8]) const {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
-  __device__ void set(const float (&f)[8]) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ void store(float* p) const {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
   }
+  __device__ float get(int i) const { return f[i]; }
+  __device__ void set2(int i, float lo, float hi) { f[i] = lo, f[i + 1] = hi; }
 };
+
+// The unit's eight planes in pairs for packed f32x2 arithmetic: members u and
+// v of planes 2i and 2i + 1 (interleaved: planes 0..3 lie in the first vector).
+struct Planes {
+  F2 u[4], v[4];
+};
+
+template <bool kHalf, typename T>
+__device__ __forceinline__ void get_planes(const Raw8<T> (&x)[2], Planes& p) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kHalf) {
+      p.u[i] = F2{x[0].get(2 * i), x[0].get(2 * i + 1)};
+      p.v[i] = F2{x[1].get(2 * i), x[1].get(2 * i + 1)};
+    } else {
+      const Raw8<T>& r = x[i >> 1];
+      const int j = 4 * (i & 1);
+      p.u[i] = F2{r.get(j), r.get(j + 2)};
+      p.v[i] = F2{r.get(j + 1), r.get(j + 3)};
+    }
+  }
+}
+
+template <bool kHalf, typename T>
+__device__ __forceinline__ void set_planes(Raw8<T> (&x)[2], const Planes& p) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kHalf) {
+      x[0].set2(2 * i, p.u[i].x, p.u[i].y);
+      x[1].set2(2 * i, p.v[i].x, p.v[i].y);
+    } else {
+      const int j = 4 * (i & 1);
+      x[i >> 1].set2(j, p.u[i].x, p.v[i].x);
+      x[i >> 1].set2(j + 2, p.u[i].y, p.v[i].y);
+    }
+  }
+}
+
+// Cosines and sines of the unit's planes, from a row of the table.
+template <bool kHalf>
+__device__ __forceinline__ void load_turns(const float* __restrict__ row, int a, int b, bool turn_a,
+                                           bool turn_b, float sign, F2 (&cs)[4], F2 (&sn)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool on = kHalf || i < 2 ? turn_a : turn_b;
+    if (on) {
+      const int at = kHalf ? 2 * a + 4 * i : (i < 2 ? a : b) + 4 * (i & 1);
+      const float4 w = __ldg(reinterpret_cast<const float4*>(row + at));
+      cs[i] = F2{w.x, w.z};
+      sn[i] = F2{sign * w.y, sign * w.w};
+    }
+  }
+}
+
+template <bool kHalf>
+__device__ __forceinline__ void turn(Planes& p, const F2 (&cs)[4], const F2 (&sn)[4], bool turn_a,
+                                     bool turn_b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool on = kHalf || i < 2 ? turn_a : turn_b;
+    if (on) {
+      const F2 u = p.u[i], v = p.v[i];
+      const F2 m = F2{-sn[i].x, -sn[i].y};
+      p.u[i] = fma_x2(u, cs[i], mul_x2(v, m));
+      p.v[i] = fma_x2(v, cs[i], mul_x2(u, sn[i]));
+    }
+  }
+}
 
 // ------------------------------------------------------------ rotation alone
 struct RopeParams {
@@ -176,60 +225,60 @@ struct RopeParams {
   const float* table;
   const int32_t* pos;    // table row of each row, or null: its own number
   int n, heads, P, rot;
-  bool half_layout, inverse;
+  float sign;            // -1: the inverse
   int* flag;
 };
 
 // kBatch steps of 512/d heads are loaded before the first is stored (out may be
 // x, so the compiler cannot move a load over a store): enough bytes in flight
 // to cover the latency of HBM.
-template <typename T, int HD>
-__global__ void __launch_bounds__(32 * kRowWarps) k_rope(RopeParams p) {
+template <typename T, int HD, bool kHalf>
+__global__ void __launch_bounds__(32 * kRowWarps) k_rope(const __grid_constant__ RopeParams p) {
   constexpr int U = HD / 16, HG = 32 / U, kBatch = sizeof(T) == 2 ? 4 : 2;
   const int lane = threadIdx.x & 31;
   const int m = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   if (m >= p.n) return;
   const int u = lane % U, h0 = lane / U;
-  const int32_t row = p.pos == nullptr ? m : __ldg(p.pos + m);
-  if (!row_ok(row, p.P, p.flag)) return;
-  const bool turned = 16 * u < p.rot;
-  int a, b;
-  unit_places(u, p.rot, p.half_layout, a, b);
+  const Places<HD, kHalf> at(u, p.rot);
   const T* x = static_cast<const T*>(p.x) + m * p.ld_x;
   T* out = static_cast<T*>(p.out) + m * p.ld_out;
-  float cs[8], sn[8];
-  if (turned) load_turns(p.table, row, p.rot, u, p.inverse, cs, sn);
+  const int32_t row = p.pos == nullptr ? m : __ldg(p.pos + m);
+  if (!row_ok(row, p.P, p.flag)) return;
+  F2 cs[4], sn[4];
+  load_turns<kHalf>(p.table + static_cast<int64_t>(row) * p.rot, at.a, at.b, at.turn_a, at.turn_b,
+                    p.sign, cs, sn);
   for (int hb = h0; hb < p.heads; hb += HG * kBatch) {
     Raw8<T> raw[kBatch][2];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int h = hb + k * HG;
       if (h < p.heads) {
-        raw[k][0].load(x + h * HD + a);
-        raw[k][1].load(x + h * HD + b);
+        raw[k][0].load(x + h * HD + at.a);
+        raw[k][1].load(x + h * HD + at.b);
       }
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int h = hb + k * HG;
       if (h >= p.heads) break;
-      if (turned) {
-        float f[2][8];
-        raw[k][0].get(f[0]);
-        raw[k][1].get(f[1]);
-        turn(f, cs, sn, p.half_layout);
-        raw[k][0].set(f[0]);
-        raw[k][1].set(f[1]);
+      if (at.turn_a) {  // without turns a value is copied bit for bit
+        Raw8<T> y[2] = {raw[k][0], raw[k][1]};
+        Planes f;
+        get_planes<kHalf>(raw[k], f);
+        turn<kHalf>(f, cs, sn, at.turn_a, at.turn_b);
+        set_planes<kHalf>(y, f);
+        raw[k][0] = y[0];
+        if (at.turn_b) raw[k][1] = y[1];
       }
-      raw[k][0].store(out + h * HD + a);
-      raw[k][1].store(out + h * HD + b);
+      raw[k][0].store(out + h * HD + at.a);
+      raw[k][1].store(out + h * HD + at.b);
     }
   }
 }
 
 // ------------------------------------------------------------ norm, rotation, cache write
 struct QkParams {
-  const __nv_bfloat16 *q_in, *k_in, *v_in;  // sources; k_in null with do_k: cache rows in place
+  const __nv_bfloat16 *q_in, *k_in, *v_in;  // sources; k_in null with k_cache: cache rows in place
   int64_t ld_q, ld_k, ld_v;
   __nv_bfloat16 *q, *k_cache, *v_cache;
   const float *w_q, *w_k;
@@ -238,16 +287,43 @@ struct QkParams {
   int n, N, P, H, rot, norm, parts;
   uint8_t part[3];  // what each of the `parts` warps of a row does: 0 q, 1 k, 2 v
   float eps;
-  bool half_layout;
   int* flag;
 };
+
+// Weights of the unit's places, arranged as its planes.
+template <bool kHalf>
+__device__ __forceinline__ void load_weights(const float* __restrict__ w, int a, int b, Planes& g) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kHalf) {
+      if (i & 1) continue;
+      const float4 x = __ldg(reinterpret_cast<const float4*>(w + a + 2 * i));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(w + b + 2 * i));
+      g.u[i] = F2{x.x, x.y}, g.u[i + 1] = F2{x.z, x.w};
+      g.v[i] = F2{y.x, y.y}, g.v[i + 1] = F2{y.z, y.w};
+    } else {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(w + (i < 2 ? a : b) + 4 * (i & 1)));
+      g.u[i] = F2{x.x, x.z}, g.v[i] = F2{x.y, x.w};
+    }
+  }
+}
+
+__device__ __forceinline__ float square_sum(const Planes& f) {
+  F2 s = mul_x2(f.u[0], f.u[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma_x2(f.u[i], f.u[i], s);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = fma_x2(f.v[i], f.v[i], s);
+  return s.x + s.y;
+}
 
 // One warp per row and part, NIT steps of 512/d heads, the whole row in
 // registers between its one read and its one write.  The mean square is
 // summed in 32 bits: over a head by shuffles between the head's lanes, over
 // the row by all lanes.  One rounding to bf16, at the store.
-template <int HD, int NIT>
-__global__ void __launch_bounds__(32 * kQkWarps) k_qk_norm_rope(const __grid_constant__ QkParams p) {
+template <int HD, int NIT, bool kHalf>
+__global__ void __launch_bounds__(32 * kQkWarps, NIT <= 3 ? 6 : 1)
+    k_qk_norm_rope(const __grid_constant__ QkParams p) {
   constexpr int U = HD / 16, HG = 32 / U;
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kQkWarps + (threadIdx.x >> 5);
@@ -258,28 +334,37 @@ __global__ void __launch_bounds__(32 * kQkWarps) k_qk_norm_rope(const __grid_con
   const int u = lane % U, h0 = lane / U;
 
   const int32_t r = p.idx == nullptr ? m : __ldg(p.idx + m);
-  const int32_t at = p.pos == nullptr ? r : __ldg(p.pos + m);
-  bool good = row_ok(r, p.N, p.flag);
-  if (p.table != nullptr && part != 2) good = row_ok(at, p.P, p.flag) && good;
-  const __nv_bfloat16* src;
-  __nv_bfloat16* dst;
-  const float* w = nullptr;
-  if (part == 0) {
-    src = p.q_in + m * p.ld_q;
-    dst = p.q + static_cast<int64_t>(m) * D;
-    w = p.w_q;
-  } else if (part == 1) {
-    if (p.k_in == nullptr && m > 0 && p.idx != nullptr && __ldg(p.idx + m - 1) >= r) {
-      // in place, a row named twice would be turned twice: the list must ascend
-      if (lane == 0) atomicOr(p.flag, DEV_BAD_INDEX);
-      good = false;
+  const int32_t trow = p.pos == nullptr ? r : __ldg(p.pos + m);
+  // The sources' rows do not depend on idx: their loads go out before its
+  // value is waited for (in place they do, and follow it).
+  const bool in_place = part == 1 && p.k_in == nullptr;
+  const __nv_bfloat16* src = part == 0 ? p.q_in + m * p.ld_q
+                             : part == 2 ? p.v_in + m * p.ld_v : p.k_in + m * p.ld_k;
+  const bool rotating = p.table != nullptr && part != 2;
+  const Places<HD, kHalf> at(u, rotating ? p.rot : 0);
+  Raw8<__nv_bfloat16> raw[NIT][2];
+  auto load_row = [&]() {
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      const int h = h0 + it * HG;
+      raw[it][0].zero();
+      raw[it][1].zero();
+      if (h < p.H) {
+        raw[it][0].load(src + h * HD + at.a);
+        raw[it][1].load(src + h * HD + at.b);
+      }
     }
-    dst = p.k_cache + static_cast<int64_t>(r) * D;
-    src = p.k_in != nullptr ? p.k_in + m * p.ld_k : dst;
-    w = p.w_k;
-  } else {
-    dst = p.v_cache + static_cast<int64_t>(r) * D;
-    src = p.v_in + m * p.ld_v;
+  };
+  if (!in_place) load_row();
+  bool good = row_ok(r, p.N, p.flag);
+  if (rotating) good = row_ok(trow, p.P, p.flag) && good;
+  __nv_bfloat16* dst = part == 0 ? p.q + static_cast<int64_t>(m) * D
+                                 : (part == 1 ? p.k_cache : p.v_cache) + static_cast<int64_t>(r) * D;
+  const float* w = part == 0 ? p.w_q : p.w_k;
+  if (in_place && m > 0 && p.idx != nullptr && __ldg(p.idx + m - 1) >= r) {
+    // a row named twice would be turned twice: the list must ascend
+    if (lane == 0) atomicOr(p.flag, DEV_BAD_INDEX);
+    good = false;
   }
   if (!good) {  // skipped and reported; a query row is left zero rather than unset
     if (part == 0)
@@ -287,106 +372,103 @@ __global__ void __launch_bounds__(32 * kQkWarps) k_qk_norm_rope(const __grid_con
         *reinterpret_cast<uint4*>(dst + e) = make_uint4(0u, 0u, 0u, 0u);
     return;
   }
-  const bool turned = p.table != nullptr && part != 2 && 16 * u < p.rot;
-  int a, b;
-  unit_places(u, p.table != nullptr && part != 2 ? p.rot : 0, p.half_layout, a, b);
-  Raw8<__nv_bfloat16> raw[NIT][2];
-#pragma unroll
-  for (int it = 0; it < NIT; ++it) {
-    const int h = h0 + it * HG;
-    raw[it][0].w = raw[it][1].w = make_uint4(0u, 0u, 0u, 0u);
-    if (h < p.H) {
-      raw[it][0].load(src + h * HD + a);
-      raw[it][1].load(src + h * HD + b);
-    }
+  if (in_place) {
+    src = dst;
+    load_row();
   }
-  if (part == 2) {  // values go to the cache as they are
+  const bool per_head = p.norm == HSA_NORM_HEAD, per_row = p.norm == HSA_NORM_ROW;
+  const bool plain = part == 2 || (p.norm == HSA_NORM_NONE && !rotating);
+  if (!plain) {
+    F2 cs[4], sn[4];
+    if (rotating)
+      load_turns<kHalf>(p.table + static_cast<int64_t>(trow) * p.rot, at.a, at.b, at.turn_a,
+                        at.turn_b, 1.0f, cs, sn);
+    Planes g;  // weights of a norm over each head: the same for all heads
+    const bool weighted = w != nullptr && p.norm != HSA_NORM_NONE;
+    if (weighted && per_head) load_weights<kHalf>(w, at.a, at.b, g);
+    float row_scale = 1.0f;
+    if (per_row) {
+      float ss = 0.f;
+#pragma unroll
+      for (int it = 0; it < NIT; ++it) {
+        Planes f;
+        get_planes<kHalf>(raw[it], f);
+        ss += square_sum(f);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      row_scale = rsqrtf(ss / static_cast<float>(D) + p.eps);
+    }
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
       const int h = h0 + it * HG;
+      Planes f;
+      get_planes<kHalf>(raw[it], f);
+      if (p.norm != HSA_NORM_NONE) {
+        float scale = row_scale;
+        if (per_head) {
+          float ss = square_sum(f);
+#pragma unroll
+          for (int o = U / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          scale = rsqrtf(ss * (1.0f / HD) + p.eps);
+        }
+        if (weighted && per_row && h < p.H) load_weights<kHalf>(w + h * HD, at.a, at.b, g);
+        const F2 s2 = splat(scale);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f.u[i] = mul_x2(f.u[i], s2);
+          f.v[i] = mul_x2(f.v[i], s2);
+          if (weighted) {
+            f.u[i] = mul_x2(f.u[i], g.u[i]);
+            f.v[i] = mul_x2(f.v[i], g.v[i]);
+          }
+        }
+      }
+      if (rotating) turn<kHalf>(f, cs, sn, at.turn_a, at.turn_b);
+      set_planes<kHalf>(raw[it], f);
       if (h < p.H) {
-        raw[it][0].store(dst + h * HD + a);
-        raw[it][1].store(dst + h * HD + b);
+        raw[it][0].store(dst + h * HD + at.a);
+        raw[it][1].store(dst + h * HD + at.b);
       }
     }
     return;
   }
-  float cs[8], sn[8];
-  if (turned) load_turns(p.table, at, p.rot, u, false, cs, sn);
-  float g[2][8];  // weights of a norm over each head: the same for all heads
-  const bool per_head = p.norm == HSA_NORM_HEAD, weighted = w != nullptr && p.norm != HSA_NORM_NONE;
-  if (weighted && per_head) {
-    load8(w + a, g[0]);
-    load8(w + b, g[1]);
-  }
-  float row_scale = 1.0f;
-  if (p.norm == HSA_NORM_ROW) {
-    float ss = 0.f;
 #pragma unroll
-    for (int it = 0; it < NIT; ++it)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float f[8];
-        raw[it][k].get(f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    row_scale = rsqrtf(ss / static_cast<float>(D) + p.eps);
-  }
-#pragma unroll
-  for (int it = 0; it < NIT; ++it) {
+  for (int it = 0; it < NIT; ++it) {  // values go to the cache as they are
     const int h = h0 + it * HG;
-    float f[2][8];
-    raw[it][0].get(f[0]);
-    raw[it][1].get(f[1]);
-    if (p.norm != HSA_NORM_NONE) {
-      float scale = row_scale;
-      if (per_head) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[0][i], f[0][i], fmaf(f[1][i], f[1][i], ss));
-#pragma unroll
-        for (int o = U / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        scale = rsqrtf(ss * (1.0f / HD) + p.eps);
-      }
-      if (weighted && !per_head && h < p.H) {
-        load8(w + h * HD + a, g[0]);
-        load8(w + h * HD + b, g[1]);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[k][i] *= scale;
-          if (weighted) f[k][i] *= g[k][i];
-        }
-    }
-    if (turned) turn(f, cs, sn, p.half_layout);
-    raw[it][0].set(f[0]);
-    raw[it][1].set(f[1]);
     if (h < p.H) {
-      raw[it][0].store(dst + h * HD + a);
-      raw[it][1].store(dst + h * HD + b);
+      raw[it][0].store(dst + h * HD + at.a);
+      raw[it][1].store(dst + h * HD + at.b);
     }
   }
 }
 
-template <int HD>
-cudaError_t launch_qk(const Ctx& c, const QkParams& p) {
-  constexpr int HG = 512 / HD;
-  const int nit = (p.H + HG - 1) / HG;
+template <int HD, int NIT>
+void qk_kernel(const Ctx& c, const QkParams& p, bool half_layout) {
   const int64_t items = static_cast<int64_t>(p.n) * p.parts;
   const unsigned grid = static_cast<unsigned>((items + kQkWarps - 1) / kQkWarps);
-  const dim3 block(32 * kQkWarps);
-  if (nit <= 1) k_qk_norm_rope<HD, 1><<<grid, block, 0, c.stream>>>(p);
-  else if (nit <= 3) k_qk_norm_rope<HD, 3><<<grid, block, 0, c.stream>>>(p);
-  else if (nit <= 6) k_qk_norm_rope<HD, 6><<<grid, block, 0, c.stream>>>(p);
-  else if (nit <= 10) k_qk_norm_rope<HD, 10><<<grid, block, 0, c.stream>>>(p);
-  else k_qk_norm_rope<HD, kMaxQkSteps><<<grid, block, 0, c.stream>>>(p);
+  if (half_layout) k_qk_norm_rope<HD, NIT, true><<<grid, 32 * kQkWarps, 0, c.stream>>>(p);
+  else k_qk_norm_rope<HD, NIT, false><<<grid, 32 * kQkWarps, 0, c.stream>>>(p);
+}
+
+template <int HD>
+cudaError_t launch_qk(const Ctx& c, const QkParams& p, bool half_layout) {
+  constexpr int HG = 512 / HD;
+  const int nit = (p.H + HG - 1) / HG;
+  if (nit <= 1) qk_kernel<HD, 1>(c, p, half_layout);
+  else if (nit <= 3) qk_kernel<HD, 3>(c, p, half_layout);
+  else if (nit <= 6) qk_kernel<HD, 6>(c, p, half_layout);
+  else if (nit <= 10) qk_kernel<HD, 10>(c, p, half_layout);
+  else qk_kernel<HD, kMaxQkSteps>(c, p, half_layout);
   c.launches += 1;
   return cudaGetLastError();
+}
+
+template <typename T, int HD>
+void rope_kernel(const Ctx& c, const RopeParams& p, bool half_layout) {
+  const unsigned grid = (p.n + kRowWarps - 1) / kRowWarps;
+  if (half_layout) k_rope<T, HD, true><<<grid, 32 * kRowWarps, 0, c.stream>>>(p);
+  else k_rope<T, HD, false><<<grid, 32 * kRowWarps, 0, c.stream>>>(p);
 }
 
 }  // namespace
@@ -395,7 +477,7 @@ cudaError_t launch_rope_table(const Ctx& c, const RopeFreqs& f, const int32_t* p
                               float* table) {
   Timed timed(c, TC_ROWS, static_cast<double>(P) * (8.0 * f.half + 4.0 * f.n_axes));
   TableParams p{};
-  for (int i = 0; i < f.half; ++i) p.turns[i] = f.turns[i], p.axis[i] = f.axis[i];
+  for (int i = 0; i < f.half; ++i) p.quarters[i] = f.quarters[i], p.axis[i] = f.axis[i];
   p.pos = pos;
   p.n_axes = f.n_axes;
   p.P = P;
@@ -415,13 +497,11 @@ cudaError_t launch_rope(const Ctx& c, const void* x, int64_t ld_x, bool f32, int
                         bool inverse, void* out, int64_t ld_out) {
   const int hd = c.cfg.D / c.cfg.H;
   Timed timed(c, TC_ROWS, static_cast<double>(n) * ((f32 ? 8.0 : 4.0) * heads * hd + 4.0 * rot));
-  RopeParams p{x, out, ld_x, ld_out, table, pos, n, heads, P, rot, half_layout, inverse, c.flag};
-  const unsigned grid = (n + kRowWarps - 1) / kRowWarps;
-  const dim3 block(32 * kRowWarps);
-  if (f32 && hd == 128) k_rope<float, 128><<<grid, block, 0, c.stream>>>(p);
-  else if (f32) k_rope<float, 64><<<grid, block, 0, c.stream>>>(p);
-  else if (hd == 128) k_rope<__nv_bfloat16, 128><<<grid, block, 0, c.stream>>>(p);
-  else k_rope<__nv_bfloat16, 64><<<grid, block, 0, c.stream>>>(p);
+  const RopeParams p{x, out, ld_x, ld_out, table, pos, n, heads, P, rot, inverse ? -1.0f : 1.0f, c.flag};
+  if (f32 && hd == 128) rope_kernel<float, 128>(c, p, half_layout);
+  else if (f32) rope_kernel<float, 64>(c, p, half_layout);
+  else if (hd == 128) rope_kernel<__nv_bfloat16, 128>(c, p, half_layout);
+  else rope_kernel<__nv_bfloat16, 64>(c, p, half_layout);
   c.launches += 1;
   return cudaGetLastError();
 }
@@ -455,9 +535,10 @@ cudaError_t launch_qk_norm_rope(const Ctx& c, const hsa_qk_rope& a, const QkRows
   p.rot = a.rot;
   p.norm = a.norm;
   p.eps = a.eps;
-  p.half_layout = a.layout == HSA_ROPE_HALF;
   p.flag = c.flag;
-  return hd == 128 ? launch_qk<128>(c, p) : launch_qk<64>(c, p);
+  // (without a table the layout only says where a unit's vectors lie)
+  const bool half_layout = a.layout == HSA_ROPE_HALF;
+  return hd == 128 ? launch_qk<128>(c, p, half_layout) : launch_qk<64>(c, p, half_layout);
 }
 
 }  // namespace hsa
