@@ -838,7 +838,7 @@ hsa_status hsa_rope_table(hsa_ctx* ctx, const hsa_rope_cfg* cfg, const int32_t* 
         keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
         w = (1.0 - keep) * w / c.factor + keep * w;
       }
-      f.quarters[j] = w / (kTwoPi / 4.0);
+      f.turns[j] = static_cast<uint64_t>(ldexp(w / kTwoPi, 64));  // w <= 1
       f.axis[j] = static_cast<uint8_t>(x);
     }
   }

@@ -212,8 +212,8 @@ cudaError_t launch_attention(const Ctx& c, const void* q, int n, const void* kc,
 
 // Rotary frequencies as the table kernel takes them.
 struct RopeFreqs {
-  double quarters[kMaxRopePairs];  // frequency of each plane, quarter turns per position
-  uint8_t axis[kMaxRopePairs];     // position axis of each plane
+  uint64_t turns[kMaxRopePairs];  // frequency of each plane, turns per position * 2^64
+  uint8_t axis[kMaxRopePairs];    // position axis of each plane
   int half, n_axes;
   float amp;
 };

@@ -31,63 +31,106 @@ constexpr int kQkWarps = 4;   // rows are wide in registers: small blocks leave 
 
 // ------------------------------------------------------------ table
 struct TableParams {
-  double quarters[kMaxRopePairs];  // frequency of each plane in quarter turns per position
+  uint64_t turns[kMaxRopePairs];  // frequency of each plane: turns per position * 2^64
   uint8_t axis[kMaxRopePairs];
-  const int32_t* pos;              // [P, n_axes], or null: row p has position p
+  const int32_t* pos;             // [P, n_axes], or null: row p has position p
   int n_axes, P, half;
   float amp;
-  float2* table;                   // [P, half]
+  float2* table;                  // [P, half]
 };
 
-// table[p][i] = amp (cos, sin)(pos f_i).  The angle is held in 64 bits, as
-// quarter turns: pos * quarters = k + r with k whole and |r| <= 1/2.  Only r
-// and k mod 4 matter, and r is taken before anything is rounded to 32 bits, so
-// far positions lose nothing (at 2^20, r is good to 2^-32 of a turn).  Adding 1.5 * 2^52
-// leaves k in the low bits of the sum, which is exact below 2^51 quarter
-// turns; a 32-bit position and f <= 1 stay below 2^32.  Sine and cosine of
-// x = r pi / 2, |x| <= pi / 4, are their Taylor polynomials to x^9 and x^10
-// (the next terms are below 2e-9), and k mod 4 swaps and negates them.
-// Four 64-bit operations per entry instead of a 64-bit sine and cosine.
-// A thread keeps one plane and walks over rows, the positions of kTableBatch
-// of them loaded together: block (half, 256 / half).
-constexpr int kTableBatch = 4;
+// table[p][i] = amp (cos, sin)(pos f_i).  The angle is a fixed-point count of
+// 2^-64 turns, so pos * turns wraps at whole turns by itself and far positions
+// lose nothing: the frequency's rounding, 2^-65 turns, grows with the position
+// to 2^-34 of a turn at most.  The nearest quarter turn k is taken off, and sine and cosine of
+// the rest x, |x| <= pi / 4, are their Taylor polynomials to x^9 and x^10
+// (the next terms are below 2e-9); k mod 4 swaps and negates them.
+//
+// A thread keeps two planes and walks over the rows of its block's share: one
+// position and one address serve both, and the polynomials run on packed
+// f32x2 (69 issued instructions an entry with one plane and 64-bit sines).
+// The positions of kTableRows rows are brought to shared memory together: a
+// load per row left every row waiting for HBM on its own.
+constexpr int kTableRows = 256;
 
+struct Quarter {
+  uint32_t k;  // nearest quarter turn
+  float x;     // what is left, in radians
+};
+
+__device__ __forceinline__ Quarter quarter_of(int32_t at, uint64_t turns) {
+  const uint32_t t =
+      static_cast<uint32_t>((static_cast<uint64_t>(static_cast<int64_t>(at)) * turns) >> 32);
+  const uint32_t k = (t + 0x20000000u) >> 30;  // an eighth of a turn up, then down to a quarter
+  return Quarter{k, static_cast<float>(static_cast<int32_t>(t - (k << 30))) * 1.4629180792671596e-9f};  // 2 pi 2^-32
+}
+
+// (cos, sin) of a quarter count and the rest's (cos, sin).
+__device__ __forceinline__ float2 unfold(uint32_t k, float c, float s) {
+  const float u = (k & 1) ? s : c, v = (k & 1) ? c : s;
+  return make_float2(__uint_as_float(__float_as_uint(u) ^ (((k + 1) & 2u) << 30)),
+                     __uint_as_float(__float_as_uint(v) ^ ((k & 2u) << 30)));
+}
+
+// Block (half / kPlanes, 256 / that); an odd count of planes takes one a thread.
+template <int kPlanes>
 __global__ void __launch_bounds__(256) k_rope_table(const __grid_constant__ TableParams p) {
-  constexpr double kRound = 6755399441055744.0;  // 1.5 * 2^52
-  const int i = threadIdx.x;
-  const double quarters = p.quarters[i];
-  const int axis = p.axis[i];
-  const int stride = gridDim.x * blockDim.y;
-  for (int64_t row0 = blockIdx.x * blockDim.y + threadIdx.y; row0 < p.P;
-       row0 += kTableBatch * static_cast<int64_t>(stride)) {
-    int32_t at[kTableBatch];
-#pragma unroll
-    for (int n = 0; n < kTableBatch; ++n) {
-      const int64_t row = row0 + n * static_cast<int64_t>(stride);
-      at[n] = row >= p.P ? 0 : p.pos == nullptr ? static_cast<int32_t>(row)
-                                                : __ldg(p.pos + row * p.n_axes + axis);
+  // The frequencies are kernel arguments: a warp reads them one at a time, as a
+  // constant that differs between lanes is fetched once per lane.
+  __shared__ uint64_t s_turns[kMaxRopePairs];
+  __shared__ int s_axis[kMaxRopePairs];
+  __shared__ int32_t s_pos[kTableRows * 3];
+  const int thread = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
+  const int64_t P = p.P;
+  const int first = static_cast<int>(P * blockIdx.x / gridDim.x);
+  const int last = static_cast<int>(P * (blockIdx.x + 1) / gridDim.x);
+  for (int row0 = first; row0 < last; row0 += kTableRows) {
+    const int rows = min(kTableRows, last - row0);
+    __syncthreads();
+    if (p.pos != nullptr) {
+      const int32_t* src = p.pos + static_cast<int64_t>(row0) * p.n_axes;
+      for (int j = thread; j < rows * p.n_axes; j += threads) s_pos[j] = __ldg(src + j);
+    } else {
+      for (int j = thread; j < rows; j += threads) s_pos[j] = row0 + j;
     }
-#pragma unroll
-    for (int n = 0; n < kTableBatch; ++n) {
-      const int64_t row = row0 + n * static_cast<int64_t>(stride);
-      if (row >= p.P) break;
-      const double full = static_cast<double>(at[n]) * quarters;
-      const double shifted = full + kRound;
-      const int k = __double2loint(shifted);
-      const float x = static_cast<float>(full - (shifted - kRound)) * 1.5707963267948966f;
-      const float z = x * x;
-      float s = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
-      s = fmaf(z, s, 1.f / 120.f);
-      s = fmaf(z, s, -1.f / 6.f);
-      s = fmaf(x * z, s, x);
-      float c = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
-      c = fmaf(z, c, -1.f / 720.f);
-      c = fmaf(z, c, 1.f / 24.f);
-      c = fmaf(z, c, -0.5f);
-      c = fmaf(z, c, 1.f);
-      const float u = (k & 1) ? s : c, v = (k & 1) ? c : s;
-      const float cs = ((k + 1) & 2) ? -u : u, sn = (k & 2) ? -v : v;
-      p.table[row * p.half + i] = make_float2(p.amp * cs, p.amp * sn);
+    if (row0 == first && (thread & 31) == 0) {
+      for (int j = thread >> 5; j < p.half; j += (threads + 31) >> 5) {
+        s_turns[j] = p.turns[j];
+        s_axis[j] = p.axis[j];
+      }
+    }
+    __syncthreads();
+    const int i = kPlanes * threadIdx.x;
+    const uint64_t turns0 = s_turns[i], turns1 = s_turns[i + kPlanes - 1];
+    const int32_t* pos0 = s_pos + s_axis[i];
+    const int32_t* pos1 = s_pos + s_axis[i + kPlanes - 1];
+    const F2 amp = splat(p.amp);
+    float2* out = p.table + static_cast<int64_t>(row0) * p.half + i;
+#pragma unroll 2
+    for (int row = threadIdx.y; row < rows; row += blockDim.y) {
+      const Quarter q0 = quarter_of(pos0[row * p.n_axes], turns0);
+      const Quarter q1 = kPlanes == 2 ? quarter_of(pos1[row * p.n_axes], turns1) : q0;
+      const F2 x = F2{q0.x, q1.x};
+      const F2 z = mul_x2(x, x);
+      F2 s = fma_x2(z, splat(1.f / 362880.f), splat(-1.f / 5040.f));
+      s = fma_x2(z, s, splat(1.f / 120.f));
+      s = fma_x2(z, s, splat(-1.f / 6.f));
+      s = fma_x2(mul_x2(x, z), s, x);
+      F2 c = fma_x2(z, splat(-1.f / 3628800.f), splat(1.f / 40320.f));
+      c = fma_x2(z, c, splat(-1.f / 720.f));
+      c = fma_x2(z, c, splat(1.f / 24.f));
+      c = fma_x2(z, c, splat(-0.5f));
+      c = fma_x2(z, c, splat(1.f));
+      s = mul_x2(s, amp);
+      c = mul_x2(c, amp);
+      const float2 t0 = unfold(q0.k, c.x, s.x);
+      float2* dst = out + static_cast<int64_t>(row) * p.half;
+      if (kPlanes == 2) {
+        const float2 t1 = unfold(q1.k, c.y, s.y);
+        __stcs(reinterpret_cast<float4*>(dst), make_float4(t0.x, t0.y, t1.x, t1.y));
+      } else {
+        *dst = t0;
+      }
     }
   }
 }
@@ -477,17 +520,21 @@ cudaError_t launch_rope_table(const Ctx& c, const RopeFreqs& f, const int32_t* p
                               float* table) {
   Timed timed(c, TC_ROWS, static_cast<double>(P) * (8.0 * f.half + 4.0 * f.n_axes));
   TableParams p{};
-  for (int i = 0; i < f.half; ++i) p.quarters[i] = f.quarters[i], p.axis[i] = f.axis[i];
+  for (int i = 0; i < f.half; ++i) p.turns[i] = f.turns[i], p.axis[i] = f.axis[i];
   p.pos = pos;
   p.n_axes = f.n_axes;
   p.P = P;
   p.half = f.half;
   p.amp = f.amp;
   p.table = reinterpret_cast<float2*>(table);
-  const dim3 block(f.half, 256 / f.half);
-  int64_t blocks = (static_cast<int64_t>(P) + block.y - 1) / block.y;
+  const int planes = f.half % 2 == 0 ? 2 : 1;  // two keep their 16-byte stores aligned
+  const dim3 block(f.half / planes, 256 / (f.half / planes));
+  // whole rounds of blocks, up to 8 on an SM, with some rows for each thread
+  int64_t blocks = (static_cast<int64_t>(P) + 4 * block.y - 1) / (4 * block.y);
   if (blocks > c.num_sms * 8) blocks = c.num_sms * 8;
-  k_rope_table<<<static_cast<unsigned>(blocks), block, 0, c.stream>>>(p);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (planes == 2) k_rope_table<2><<<grid, block, 0, c.stream>>>(p);
+  else k_rope_table<1><<<grid, block, 0, c.stream>>>(p);
   c.launches += 1;
   return cudaGetLastError();
 }
