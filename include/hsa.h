@@ -593,10 +593,10 @@ typedef struct {
   const void* k;           /* (device) bf16 [B, S, kv_heads * D/H], rows ld_k apart, */
   const void* v;           /*   sequences bs_k apart (elements); v likewise */
   int64_t ld_k, bs_k, ld_v, bs_v; /* multiples of 8; ld >= kv_heads * D/H; bs >= 0 (0: shared) */
-  int S;                   /* padded key count, >= 1 */
+  int S;                   /* padded key count, 1 .. 2^26 */
   int kv_heads;            /* divides H: query head h reads key head h / (H / kv_heads) */
   const int32_t* kv_len;   /* (device) int32 [B] keys of each sequence, in [0, S]; NULL: S */
-  const uint8_t* kv_mask;  /* (device) uint8 [B, S], 0 = key not seen; NULL: all seen.  S <= 131072 */
+  const uint8_t* kv_mask;  /* (device) uint8 [B, S], 0 = key not seen; NULL: all seen */
   float scale;             /* of the scores; 0: 1 / sqrt(D/H) */
   void* o;                 /* (device) bf16 [n, D] out, rows of the sequences only */
 } hsa_cross_args;

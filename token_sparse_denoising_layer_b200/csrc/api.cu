@@ -910,8 +910,8 @@ hsa_status hsa_cross_attention(hsa_ctx* ctx, const hsa_cross_args* a) {
   HSA_CHECK_CTX(ctx);
   if (a == nullptr) return fail(ctx, HSA_ERR_INVALID_ARG, "a is NULL");
   const int H = ctx->c.cfg.H, hd = ctx->c.cfg.D / H;
-  if (a->n < 0 || a->B < 1 || a->S < 1)
-    return fail(ctx, HSA_ERR_SHAPE, "cross_attention needs n >= 0, B >= 1 and S >= 1");
+  if (a->n < 0 || a->B < 1 || a->S < 1 || a->S > hsa::kMaxCrossKeys)
+    return fail(ctx, HSA_ERR_SHAPE, "cross_attention needs n >= 0, B >= 1 and 1 <= S <= 2^26");
   if (a->kv_heads < 1 || H % a->kv_heads != 0)
     return fail(ctx, HSA_ERR_SHAPE, "kv_heads must divide H");
   const int64_t width = static_cast<int64_t>(a->kv_heads) * hd;
@@ -921,8 +921,6 @@ hsa_status hsa_cross_attention(hsa_ctx* ctx, const hsa_cross_args* a) {
   for (int64_t bs : {a->bs_k, a->bs_v})
     if (bs < 0 || bs % 8 != 0 || bs >= (1ll << 38))
       return fail(ctx, HSA_ERR_SHAPE, "bs_k and bs_v must be multiples of 8, >= 0");
-  if (a->kv_mask != nullptr && a->S > hsa::kMaxMaskedKeys)
-    return fail(ctx, HSA_ERR_SHAPE, "a key mask takes S <= 131072");
   if (!(a->scale >= 0.f) || !isfinite(a->scale))
     return fail(ctx, HSA_ERR_INVALID_ARG, "scale must be finite and >= 0");
   if (a->n == 0) return HSA_OK;

@@ -17,7 +17,9 @@ constexpr int kMaxGroups = 8;
 constexpr int kMaxCaches = 8;  // copies of a KV cache one QKV launch can write (ranks of a step)
 constexpr int kMaxRopePairs = 64;  // planes of one head a rotary table can turn (head_dim 128)
 constexpr int kMaxQkSteps = 20;    // 512-place steps of a row the norm + rotation pass holds
-constexpr int kMaxMaskedKeys = 131072;  // keys whose mask bits fit a CTA's shared memory
+// Padded keys of a sequence: an empty mask of so many is looked through well
+// inside the time that a bounded wait allows.
+constexpr int kMaxCrossKeys = 1 << 26;
 // Longest row of an 8-bit product: 128 * 128 * 131071 still fits 32-bit sums.
 constexpr int kMaxQuantK = 131071;
 constexpr int kMaxLnQuantD = 40 * 128;  // widest row of the LayerNorm that quantises

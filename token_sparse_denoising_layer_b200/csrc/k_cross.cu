@@ -5,21 +5,32 @@
 //   o[m] = sum_j softmax_j(scale q[m] . k[b][j]) v[b][j],  b the sequence of
 // row m, over the keys j < kv_len[b] whose mask byte is set.
 //
-// The tile pipeline is that of the active-query attention (k_attn.cu): one CTA
-// works on two 128-query tiles of one head that share every 128-key tile, S
-// and O live in TMEM, P is written over S as bf16 and read from there by the
-// second product, and the two query tiles ping-pong.  What differs:
-//  - Which rows and keys a CTA owns is read on the device.  Units of 256
-//    queries are numbered per head so that sequence b's first unit is
+// Arithmetic of a tile as in the active-query attention (k_attn.cu): two
+// 128-query tiles of one head share every 128-key tile, S and O live in TMEM,
+// P is written over S as bf16 and read from there by the second product, and
+// the two query tiles ping-pong.  What differs:
+//  - One persistent CTA per SM walks over units of 256 queries x one head.  Key
+//    sets are short (a prompt is a few tiles), so a CTA per unit spent two
+//    thirds of its time on its own start and end: the next unit's descriptor, Q
+//    and first keys now arrive while this one's last tile is in softmax, and
+//    its first scores are computed under this one's epilogue.  (26207 queries,
+//    12 heads, 512 and 384 keys: 145 us with a CTA per unit.)
+//  - Which rows and keys a unit covers is read on the device.  Units are
+//    numbered per head so that sequence b's first one is
 //    floor(q_start[b] / 256) + b: every sequence has room for its last,
 //    partial unit, the host knows their number (n / 256 + B) without knowing
-//    the lengths, and a CTA finds its sequence by a search over q_start alone.
-//    Units that no row needs return at once.
+//    the lengths, and a unit's sequence is found by a search over q_start
+//    alone.  The producer warp finds the next unit that has rows and passes
+//    its descriptor to the other warps through a ring of two.
 //  - Key tiles before the first and after the last seen key are not loaded.
 //    In tiles with unseen keys the scores are replaced by -inf and the unseen
 //    rows of V are zeroed in shared memory before the product reads them: a
 //    weight of 0 would not silence a NaN there.
-//  - Rows without any key get zeros.
+//  - Rows without any key get zeros.  Warps whose 32 rows lie past the
+//    sequence's end (one query a sequence) do no softmax.
+//
+// Warp 0: descriptors and TMA.  Warp 1: TMEM owner and MMA issuer.  Warps 2..5
+// and 6..9: the softmax warpgroups of the two query tiles.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -42,21 +53,33 @@ constexpr int kQ = 128;        // queries per tile
 constexpr int kUnitQ = 2 * kQ; // queries per unit
 constexpr int kStages = 2;     // K and V ring depth
 constexpr int kThreads = 320;
+constexpr int kSoftmaxWarps = 8;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kStageBytes = 32 * 128;  // per softmax warp: 32 output rows x 64 columns
 
 template <int HD>
 struct CrossCfg {
   static constexpr int kRegions = HD / 64;                    // 128-byte column regions
   static constexpr int kRegionBytes = 128 * 128;
   static constexpr int kTileBytes = kRegions * kRegionBytes;  // one Q, K or V tile
-  static constexpr int kBitsAt = kTileBytes * (2 + 2 * kStages) + 256;
+  static constexpr int kStageAt = kTileBytes * (2 + 2 * kStages);
+  static constexpr int kBarsAt = kStageAt + kSoftmaxWarps * kStageBytes;
   // Every CTA takes all 512 TMEM columns, so only one may be resident per SM.
-  static constexpr int kSmem = HD == 64 ? 160 * 1024 : kBitsAt + 1024 + kMaxMaskedKeys / 8;
+  static constexpr int kSmem = HD == 64 ? 160 * 1024 : kBarsAt + 1024 + 512;
   static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + HD;
 };
-static_assert(CrossCfg<64>::kBitsAt + 1024 + kMaxMaskedKeys / 8 <= CrossCfg<64>::kSmem &&
+static_assert(CrossCfg<64>::kBarsAt + 1024 + 512 <= CrossCfg<64>::kSmem &&
                   CrossCfg<128>::kSmem <= 227 * 1024,
               "cross-attention exceeds the shared memory of a CTA");
+
+// What the warps of a CTA need to know of a unit (or of one key range of it).
+struct UnitDesc {
+  int q0, q1;    // rows
+  int b, h;      // sequence, query head
+  int j0, nkv;   // key tiles [j0, j0 + nkv); nkv < 0: no more units
+  int len;       // keys of the sequence
+  int part;      // index of this key range's partial result, or -1
+};
 
 struct CrossParams {
   int n, B, S, group;  // group: query heads per key head
@@ -68,9 +91,9 @@ struct CrossParams {
   const int32_t* kv_len;
   const uint8_t* kv_mask;
   int* flag;
-  // Work: units [0, n_full) of units_per_head * H whole, the rest split into
-  // `split` key ranges each, merged by k_cross_combine.
-  int units_per_head, n_full, split;
+  // Work: units_per_head * H units, each in `split` key ranges; with more than
+  // one, partial results are merged by k_cross_combine.
+  int units_per_head, units, split;
   float* part_o;
   float2* part_ml;
 };
@@ -104,17 +127,35 @@ __device__ __forceinline__ void unit_rows(const CrossParams& p, int u, int& b, i
   q1 = min(last, q0 + kUnitQ);
 }
 
-// Bits of the keys of tile j that may be seen.
-__device__ __forceinline__ void seen_bits(const uint32_t* bits, int len, int j, uint32_t (&w)[4]) {
+// Bits of the first `left` of a tile's keys.
+__device__ __forceinline__ void first_bits(int left, uint32_t (&w)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (bits != nullptr) {
-      w[i] = bits[4 * j + i];
-    } else {
-      const int left = len - j * kKV - 32 * i;
-      w[i] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
-    }
+    const int n = left - 32 * i;
+    w[i] = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
   }
+}
+
+// First and last + 1 key tiles of a sequence that hold a seen key (lo == hi:
+// none).  Executed by one warp.
+__device__ __forceinline__ void seen_tiles(const CrossParams& p, int b, int len, int& lo, int& hi) {
+  lo = 0;
+  hi = (len + kKV - 1) / kKV;
+  if (p.kv_mask == nullptr) return;
+  const int lane = threadIdx.x & 31;
+  const uint8_t* row = p.kv_mask + static_cast<int64_t>(b) * p.S;
+  // a tile per step, from the front and from the back: 4 bytes a lane
+  auto any_seen = [&](int tile) {
+    bool see = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = tile * kKV + 32 * i + lane;
+      see = see || (key < len && __ldg(row + key) != 0);
+    }
+    return __any_sync(0xffffffffu, see);
+  };
+  while (lo < hi && !any_seen(lo)) ++lo;
+  while (hi > lo && !any_seen(hi - 1)) --hi;
 }
 
 __device__ __forceinline__ void hide(uint32_t (&sr)[kKV], const uint32_t (&w)[4]) {
@@ -123,29 +164,31 @@ __device__ __forceinline__ void hide(uint32_t (&sr)[kKV], const uint32_t (&w)[4]
     if (!((w[e >> 5] >> (e & 31)) & 1u)) sr[e] = __float_as_uint(-INFINITY);
 }
 
-template <int HD>
+template <int HD, bool kMask>
 __global__ void __launch_bounds__(kThreads, 1)
     k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
             const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CrossParams p) {
   using Cfg = CrossCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_first, s_last;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;                              // [2] tiles
   uint8_t* sK = sQ + 2 * Cfg::kTileBytes;          // [kStages]
   uint8_t* sV = sK + kStages * Cfg::kTileBytes;    // [kStages]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + kStages * Cfg::kTileBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kBarsAt);
   uint64_t* q_full = bars;
-  uint64_t* k_full = q_full + 1;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* k_full = q_empty + 1;
   uint64_t* k_empty = k_full + kStages;
   uint64_t* v_full = k_empty + kStages;
   uint64_t* v_empty = v_full + kStages;
   uint64_t* s_full = v_empty + kStages;  // [2] per query tile
   uint64_t* p_full = s_full + 2;         // [2]
   uint64_t* o_done = p_full + 2;         // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
-  uint32_t* s_bits = reinterpret_cast<uint32_t*>(smem + Cfg::kBitsAt);
+  uint64_t* d_full = o_done + 2;         // [2] descriptors
+  uint64_t* d_empty = d_full + 2;        // [2]
+  UnitDesc* desc = reinterpret_cast<UnitDesc*>(d_empty + 2);  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(desc + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0) {  // one CTA looks the offsets and lengths over
@@ -155,26 +198,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a < 0 || e > p.n || a > e || len < 0 || len > p.S) atomicOr(p.flag, DEV_BAD_INDEX);
     }
   }
-  int unit, part = -1, piece = 0;
-  if (static_cast<int>(blockIdx.x) < p.n_full) {
-    unit = blockIdx.x;
-  } else {
-    part = blockIdx.x - p.n_full;
-    unit = p.n_full + part / p.split;
-    piece = part % p.split;
-  }
-  const int h = unit / p.units_per_head;
-  int b, q0, q1;
-  unit_rows(p, unit - h * p.units_per_head, b, q0, q1);
-  if (q0 >= q1) return;
-  const int len = p.kv_len != nullptr ? clamped(__ldg(p.kv_len + b), 0, p.S) : p.S;
-  const int col0 = h * HD, kcol0 = h / p.group * HD;
-  const int ntile = q0 + kQ < q1 ? 2 : 1;
-
   if (threadIdx.x == 0) {
-    s_first = 0x7fffffff;
-    s_last = -1;
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -185,6 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 4);  // one arrival per softmax warp
       mbar_init(&o_done[t], 1);
+      mbar_init(&d_full[t], 1);
+      mbar_init(&d_empty[t], 1 + kSoftmaxWarps);
     }
     fence_barrier_init();
   }
@@ -203,84 +231,93 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
 
-  // Key tiles [j0, j0 + nkv) of this CTA: from the first to the last seen key,
-  // or this part's share of them.
-  int lo_tile = 0, hi_tile = (len + kKV - 1) / kKV;
-  const uint32_t* bits = nullptr;
-  if (p.kv_mask != nullptr) {
-    const uint8_t* row = p.kv_mask + static_cast<int64_t>(b) * p.S;
-    for (int w = warp; w < 4 * hi_tile; w += kThreads / 32) {
-      const int key = 32 * w + lane;
-      const bool see = key < len && __ldg(row + key) != 0;
-      const uint32_t word = __ballot_sync(0xffffffffu, see);
+  if (warp == 0) {
+    // ------------------------------------------------------------ descriptors and TMA
+    const uint64_t keep = l2_policy_evict_last();  // a sequence's K/V is shared by its units
+    int it = 0;     // key tiles issued so far
+    int nq = 0;     // units whose Q was issued
+    int nd = 0;     // descriptors published
+    int seen_b = -1, lo_tile = 0, hi_tile = 0, seen_len = 0;
+    const int total = p.units * p.split;
+    for (int item = blockIdx.x; ok; item += gridDim.x) {
+      UnitDesc d{};
+      d.nkv = -1;
+      bool rows = true;
+      if (item < total) {
+        const int unit = item / p.split, piece = item - unit * p.split;
+        d.h = unit / p.units_per_head;
+        unit_rows(p, unit - d.h * p.units_per_head, d.b, d.q0, d.q1);
+        rows = d.q0 < d.q1;
+        if (rows) {
+          if (d.b != seen_b) {
+            seen_b = d.b;
+            seen_len = p.kv_len != nullptr ? clamped(__ldg(p.kv_len + d.b), 0, p.S) : p.S;
+            seen_tiles(p, d.b, seen_len, lo_tile, hi_tile);
+          }
+          d.len = seen_len;
+          const int all = hi_tile - lo_tile;
+          d.j0 = lo_tile + piece * all / p.split;
+          d.nkv = lo_tile + (piece + 1) * all / p.split - d.j0;
+          d.part = p.split > 1 ? item : -1;
+        }
+      }
+      if (!rows) continue;
       if (lane == 0) {
-        s_bits[w] = word;
-        if (word != 0u) {
-          atomicMin(&s_first, w);
-          atomicMax(&s_last, w);
+        const int slot = nd & 1;
+        ok = mbar_wait(&d_empty[slot], ((nd >> 1) & 1) ^ 1);
+        if (ok) {
+          desc[slot] = d;
+          mbar_arrive(&d_full[slot]);  // releases the descriptor
         }
+        const int ntile = d.q0 + kQ < d.q1 ? 2 : 1;
+        const int bk = p.k_shared ? 0 : d.b, bv = p.v_shared ? 0 : d.b;
+        const int qcol = d.h * HD, kcol = d.h / p.group * HD;
+        for (int j = 0; j < d.nkv && ok; ++j, ++it) {
+          const int s = it % kStages;
+          const uint32_t ph = ((it / kStages) & 1) ^ 1;
+          if (!mbar_wait(&k_empty[s], ph)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&k_full[s], Cfg::kTileBytes);
+          for (int r = 0; r < Cfg::kRegions; ++r)
+            tma_load_3d_hint(sK + s * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmK, &k_full[s],
+                             kcol + 64 * r, (d.j0 + j) * kKV, bk, keep);
+          if (j == 0) {
+            // Q may be replaced once the previous unit's last scores are done
+            if (!mbar_wait(q_empty, (nq & 1) ^ 1)) {
+              (void)mbar_wait(&k_full[s], (it / kStages) & 1);
+              ok = false;
+              break;
+            }
+            ++nq;
+            mbar_arrive_expect_tx(q_full, ntile * Cfg::kTileBytes);
+            for (int t = 0; t < ntile; ++t)
+              for (int r = 0; r < Cfg::kRegions; ++r)
+                tma_load_2d(sQ + t * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmQ, q_full,
+                            qcol + 64 * r, d.q0 + t * kQ);
+          }
+          if (!mbar_wait(&v_empty[s], ph)) {
+            (void)mbar_wait(&k_full[s], (it / kStages) & 1);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&v_full[s], Cfg::kTileBytes);
+          for (int r = 0; r < Cfg::kRegions; ++r)
+            tma_load_3d_hint(sV + s * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmV, &v_full[s],
+                             kcol + 64 * r, (d.j0 + j) * kKV, bv, keep);
+        }
+        if (!ok) {  // let copies already in flight land before the CTA exits
+          if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
+          for (int k = it > kStages ? it - kStages : 0; k < it; ++k) {
+            (void)mbar_wait(&k_full[k % kStages], (k / kStages) & 1);
+            (void)mbar_wait(&v_full[k % kStages], (k / kStages) & 1);
+          }
+        }
+        ++nd;
       }
-    }
-    __syncthreads();
-    bits = s_bits;
-    lo_tile = s_last < 0 ? 0 : s_first / 4;
-    hi_tile = s_last < 0 ? 0 : s_last / 4 + 1;
-  }
-  int j0 = lo_tile, nkv = hi_tile - lo_tile;
-  if (part >= 0) {
-    const int all = nkv;
-    j0 = lo_tile + piece * all / p.split;
-    nkv = lo_tile + (piece + 1) * all / p.split - j0;
-  }
-
-  if (nkv == 0) {
-    // no key in this range: zeros, or an empty part
-    for (int i = threadIdx.x; i < (q1 - q0) * (HD / 8); i += kThreads) {
-      const int r = i / (HD / 8), e = i % (HD / 8);
-      if (part < 0)
-        *reinterpret_cast<uint4*>(p.o + static_cast<size_t>(q0 + r) * p.ld + col0 + 8 * e) =
-            make_uint4(0u, 0u, 0u, 0u);
-      else if (e == 0)
-        p.part_ml[static_cast<size_t>(part) * kUnitQ + r] = make_float2(-FLT_MAX, 0.f);
-    }
-  } else if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t keep = l2_policy_evict_last();  // a sequence's K/V is shared by its units
-      const int bk = p.k_shared ? 0 : b, bv = p.v_shared ? 0 : b;
-      mbar_arrive_expect_tx(q_full, ntile * Cfg::kTileBytes);
-      for (int t = 0; t < ntile; ++t)
-        for (int r = 0; r < Cfg::kRegions; ++r)
-          tma_load_2d(sQ + t * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmQ, q_full,
-                      col0 + 64 * r, q0 + t * kQ);
-      int j = 0;
-      for (; j < nkv; ++j) {
-        const int s = j % kStages;
-        const uint32_t ph = ((j / kStages) & 1) ^ 1;
-        if (!mbar_wait(&k_empty[s], ph)) {
-          ok = false;
-          break;
-        }
-        mbar_arrive_expect_tx(&k_full[s], Cfg::kTileBytes);
-        for (int r = 0; r < Cfg::kRegions; ++r)
-          tma_load_3d_hint(sK + s * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmK, &k_full[s],
-                           kcol0 + 64 * r, (j0 + j) * kKV, bk, keep);
-        if (!mbar_wait(&v_empty[s], ph)) {
-          ok = false;
-          break;
-        }
-        mbar_arrive_expect_tx(&v_full[s], Cfg::kTileBytes);
-        for (int r = 0; r < Cfg::kRegions; ++r)
-          tma_load_3d_hint(sV + s * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmV, &v_full[s],
-                           kcol0 + 64 * r, (j0 + j) * kKV, bv, keep);
-      }
-      if (!ok) {  // let copies already in flight land before the CTA exits
-        (void)mbar_wait(q_full, 0);
-        for (int k = j > kStages ? j - kStages : 0; k < j; ++k) {
-          (void)mbar_wait(&k_full[k % kStages], (k / kStages) & 1);
-          (void)mbar_wait(&v_full[k % kStages], (k / kStages) & 1);
-        }
-      }
+      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+      if (item >= total) break;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -306,44 +343,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                        sdesc_sw128(v_addr + kk * 2048, Cfg::kRegionBytes, 1024), idPV,
                        (acc || kk > 0) ? 1u : 0u);
       };
-      ok = mbar_wait(q_full, 0) && mbar_wait(&k_full[0], 0);
-      if (ok) {
+      int it = 0, nq = 0, np0 = 0, np1 = 0;  // key tiles, units with keys, P tiles of either query tile
+      for (int nd = 0;; ++nd) {
+        if (!mbar_wait(&d_full[nd & 1], (nd >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const int nkv = desc[nd & 1].nkv;
+        const int ntile = desc[nd & 1].q0 + kQ < desc[nd & 1].q1 ? 2 : 1;
+        mbar_arrive(&d_empty[nd & 1]);
+        if (nkv < 0) break;
+        if (nkv == 0) continue;
+        ok = mbar_wait(q_full, nq & 1) && mbar_wait(&k_full[it % kStages], (it / kStages) & 1);
+        if (!ok) break;
+        ++nq;
         tc_fence_after();
         for (int t = 0; t < ntile; ++t) {
-          issue_s(t, 0);
+          issue_s(t, it % kStages);
           umma_commit(&s_full[t]);
         }
-        umma_commit(&k_empty[0]);
-      }
-      for (int j = 0; j < nkv && ok; ++j) {
-        const int s = j % kStages;
-        const int s1 = (j + 1) % kStages;
-        for (int t = 0; t < ntile && ok; ++t) {
-          // p_full[0] also says that the unseen rows of this V tile are zeroed
-          if (!mbar_wait(&p_full[t], j & 1)) {
-            ok = false;
-            break;
-          }
-          if (t == 0 && !mbar_wait(&v_full[s], (j / kStages) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          issue_pv(t, s, j > 0);
-          if (t == ntile - 1) umma_commit(&v_empty[s]);
-          if (j + 1 < nkv) {
-            if (t == 0 && !mbar_wait(&k_full[s1], ((j + 1) / kStages) & 1)) {
+        umma_commit(&k_empty[it % kStages]);
+        if (nkv == 1) umma_commit(q_empty);
+        for (int j = 0; j < nkv && ok; ++j, ++it) {
+          const int s = it % kStages;
+          const int s1 = (it + 1) % kStages;
+          for (int t = 0; t < ntile && ok; ++t) {
+            // p_full[0] also says that the unseen rows of this V tile are zeroed
+            if (!mbar_wait(&p_full[t], (t == 0 ? np0++ : np1++) & 1)) {
+              ok = false;
+              break;
+            }
+            if (t == 0 && !mbar_wait(&v_full[s], (it / kStages) & 1)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            issue_s(t, s1);
-            umma_commit(&s_full[t]);
-            if (t == ntile - 1) umma_commit(&k_empty[s1]);
-          } else {
-            umma_commit(&o_done[t]);
+            issue_pv(t, s, j > 0);
+            if (t == ntile - 1) umma_commit(&v_empty[s]);
+            if (j + 1 < nkv) {
+              if (t == 0 && !mbar_wait(&k_full[s1], ((it + 1) / kStages) & 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              issue_s(t, s1);
+              umma_commit(&s_full[t]);
+              if (t == ntile - 1) {
+                umma_commit(&k_empty[s1]);
+                if (j + 2 == nkv) umma_commit(q_empty);
+              }
+            } else {
+              umma_commit(&o_done[t]);
+            }
           }
         }
+        if (!ok) break;
       }
     }
   } else {
@@ -354,110 +408,183 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
     const uint32_t tS = tmem + lane_base + (t == 0 ? Cfg::kColS0 : Cfg::kColS1);
     const uint32_t tO = tmem + lane_base + (t == 0 ? Cfg::kColO0 : Cfg::kColO1);
-    const bool active = t < ntile;
-    float m_run = -FLT_MAX, l_run = 0.f;
-    for (int j = 0; j < nkv && active; ++j) {
-      uint32_t see[4];
-      seen_bits(bits, len, j0 + j, see);
-      const bool whole = (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu;  // same for all rows
-      if (!whole && t == 0) {
-        // unseen rows of V: whatever they hold must not meet a weight of 0
-        if (!__all_sync(0xffffffffu, mbar_wait(&v_full[j % kStages], (j / kStages) & 1))) {
-          ok = false;
-          break;
-        }
-        if (!((see[qd] >> lane) & 1u)) {
-          uint8_t* vrow = sV + (j % kStages) * Cfg::kTileBytes + row * 128;
-#pragma unroll
-          for (int r = 0; r < Cfg::kRegions; ++r)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(vrow + r * Cfg::kRegionBytes + 16 * i) =
-                  make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1))) {
+    uint8_t* stage = smem + Cfg::kStageAt + (warp - 2) * kStageBytes;
+    int it = 0, ns = 0, no = 0;  // key tiles of the CTA, S tiles and units of this query tile
+    for (int nd = 0; ok; ++nd) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&d_full[nd & 1], (nd >> 1) & 1))) {
         ok = false;
         break;
       }
-      tc_fence_after();
-      uint32_t sr[kKV];
-      tmem_ld128(tS, sr);
-      if (!whole) hide(sr, see);
-      // As in k_attn.cu: after the first tile the exponentials are taken
-      // against the running max as it stands, and only a row sum past 2^64
-      // (rare) has S read again, the max raised and O and l rescaled.  A row
-      // that has seen no key yet keeps the lowest finite max, so its first
-      // key takes that way too.
-      float m_use = m_run, alpha = 1.0f, rs;
-      if (j == 0) m_use = fmaxf(row_max(sr) * p.scale_log2, -FLT_MAX);
-      uint32_t w[kKV / 2];
-#pragma unroll 1
-      for (int pass = 0;; ++pass) {
-        rs = exp_row(sr, p.scale_log2, m_use, w);
-        const bool over = !(rs <= kSumLimit);
-        if (j == 0 || pass == 1 || !__any_sync(0xffffffffu, over)) break;
-        tmem_ld128(tS, sr);
-        if (!whole) hide(sr, see);
-        const float tmax = row_max(sr) * p.scale_log2;
-        if (over) {
-          m_use = fmaxf(tmax, m_run);
-          alpha = ex2_approx(m_run - m_use);
-        }
-#pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(tO + 32 * c, r);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-          tmem_st32(tO + 32 * c, r);
-        }
-        tmem_ld128(tS, sr);
-        if (!whole) hide(sr, see);
-      }
-      tmem_st64(tS, w);
-      l_run = l_run * alpha + rs;
-      m_run = m_use;
-      tc_fence_before();
+      const UnitDesc d = desc[nd & 1];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
-    }
-    // epilogue: O / l -> bf16 rows, or, for a key-range part, the unnormalised
-    // O with its (m, l) for k_cross_combine
-    if (active && ok) {
-      if (__all_sync(0xffffffffu, mbar_wait(&o_done[t], 0))) {
+      if (lane == 0) mbar_arrive(&d_empty[nd & 1]);
+      if (d.nkv < 0) break;
+      const int warp_row = d.q0 + t * kQ + 32 * qd;  // first row of this warp
+      if (d.nkv == 0) {  // no key in this range: zeros, or an empty part
+        const int rows = min(32, d.q1 - warp_row);
+        if (d.part >= 0) {
+          if (lane < rows)
+            p.part_ml[static_cast<size_t>(d.part) * kUnitQ + t * kQ + row] = make_float2(-FLT_MAX, 0.f);
+        } else {
+          for (int r = 0; r < rows; ++r)
+            if (lane < HD / 8)
+              *reinterpret_cast<uint4*>(p.o + static_cast<size_t>(warp_row + r) * p.ld + d.h * HD + 8 * lane) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      if (t == 1 && d.q0 + kQ >= d.q1) {  // no second query tile
+        it += d.nkv;
+        continue;
+      }
+      const bool mine = warp_row < d.q1;  // whether any of this warp's rows exists
+      const uint8_t* mrow = kMask ? p.kv_mask + static_cast<int64_t>(d.b) * p.S : nullptr;
+      // the mask bytes of a tile's keys, four a lane, loaded one tile ahead
+      uint32_t bytes[4] = {0u, 0u, 0u, 0u};
+      auto load_bytes = [&](int j) {
+        if (kMask) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = j * kKV + 32 * i + lane;
+            bytes[i] = key < d.len ? __ldg(mrow + key) : 0u;
+          }
+        }
+      };
+      load_bytes(d.j0);
+      float m_run = -FLT_MAX, l_run = 0.f;
+      for (int j = 0; j < d.nkv; ++j, ++it, ++ns) {
+        uint32_t see[4];
+        if (kMask) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) see[i] = __ballot_sync(0xffffffffu, bytes[i] != 0u);
+          if (j + 1 < d.nkv) load_bytes(d.j0 + j + 1);
+        } else {
+          first_bits(d.len - (d.j0 + j) * kKV, see);
+        }
+        const bool whole = (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu;  // same for all rows
+        if (!whole && t == 0) {
+          // unseen rows of V: whatever they hold must not meet a weight of 0
+          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[it % kStages], (it / kStages) & 1))) {
+            ok = false;
+            break;
+          }
+          const uint32_t mine4 = qd == 0 ? see[0] : qd == 1 ? see[1] : qd == 2 ? see[2] : see[3];
+          if (!((mine4 >> lane) & 1u)) {
+            uint8_t* vrow = sV + (it % kStages) * Cfg::kTileBytes + row * 128;
+#pragma unroll
+            for (int r = 0; r < Cfg::kRegions; ++r)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(vrow + r * Cfg::kRegionBytes + 16 * i) =
+                    make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], ns & 1))) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const float inv = 1.0f / l_run;
-        const int qrow = q0 + t * kQ + row;
-        __nv_bfloat16* orow = p.o + static_cast<size_t>(qrow) * p.ld + col0;
-        const size_t prow = static_cast<size_t>(part) * kUnitQ + t * kQ + row;
-        if (part >= 0 && qrow < q1) p.part_ml[prow] = make_float2(m_run, l_run);
+        if (mine) {
+          uint32_t sr[kKV];
+          tmem_ld128(tS, sr);
+          if (!whole) hide(sr, see);
+          // As in k_attn.cu: after the first tile the exponentials are taken
+          // against the running max as it stands, and only a row sum past 2^64
+          // (rare) has S read again, the max raised and O and l rescaled.  A
+          // row that has seen no key yet keeps the lowest finite max, so its
+          // first key takes that way too.
+          float m_use = m_run, alpha = 1.0f, rs;
+          if (j == 0) m_use = fmaxf(row_max(sr) * p.scale_log2, -FLT_MAX);
+          uint32_t w[kKV / 2];
+#pragma unroll 1
+          for (int pass = 0;; ++pass) {
+            rs = exp_row(sr, p.scale_log2, m_use, w);
+            const bool over = !(rs <= kSumLimit);
+            if (j == 0 || pass == 1 || !__any_sync(0xffffffffu, over)) break;
+            tmem_ld128(tS, sr);
+            if (!whole) hide(sr, see);
+            const float tmax = row_max(sr) * p.scale_log2;
+            if (over) {
+              m_use = fmaxf(tmax, m_run);
+              alpha = ex2_approx(m_run - m_use);
+            }
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32(tO + 32 * c, r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+              tmem_st32(tO + 32 * c, r);
+            }
+            tmem_ld128(tS, sr);
+            if (!whole) hide(sr, see);
+          }
+          tmem_st64(tS, w);
+          l_run = l_run * alpha + rs;
+          m_run = m_use;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
+      }
+      if (!ok) break;
+      // epilogue: O / l -> bf16 rows through this warp's stage, or, for a
+      // key-range part, the unnormalised O with its (m, l) for k_cross_combine
+      if (!__all_sync(0xffffffffu, mbar_wait(&o_done[t], no & 1))) {
+        ok = false;
+        break;
+      }
+      ++no;
+      if (!mine) continue;
+      tc_fence_after();
+      if (d.part >= 0) {
+        const size_t prow = static_cast<size_t>(d.part) * kUnitQ + t * kQ + row;
+        const bool real = warp_row + lane < d.q1;
+        if (real) p.part_ml[prow] = make_float2(m_run, l_run);
 #pragma unroll 1
         for (int c = 0; c < HD / 32; ++c) {
           uint32_t r[32];
           __syncwarp();
           tmem_ld32(tO + 32 * c, r);
-          if (qrow >= q1) continue;
-          if (part >= 0) {
+          if (real) {
             float4* d4 = reinterpret_cast<float4*>(p.part_o + prow * HD + 32 * c);
 #pragma unroll
             for (int v = 0; v < 8; ++v)
               d4[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
                                   __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
-          } else {
-            uint4* d4 = reinterpret_cast<uint4*>(orow + 32 * c);
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              d4[v] = make_uint4(
-                  pack_bf16(__uint_as_float(r[8 * v]) * inv, __uint_as_float(r[8 * v + 1]) * inv),
-                  pack_bf16(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv),
-                  pack_bf16(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv),
-                  pack_bf16(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv));
           }
         }
       } else {
-        ok = false;
+        const float inv = 1.0f / l_run;
+        const int g = lane & 7;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(tO + 32 * c, r);
+          // this lane's row of the stage: 64 columns, 16-byte group v at v ^ (row & 7)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + 16 * ((4 * (c & 1) + v) ^ (lane & 7))) = make_uint4(
+                pack_bf16(__uint_as_float(r[8 * v]) * inv, __uint_as_float(r[8 * v + 1]) * inv),
+                pack_bf16(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv),
+                pack_bf16(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv),
+                pack_bf16(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv));
+          if (c & 1) {
+            // one store covers four rows and 128 contiguous bytes of each
+            __syncwarp();
+            __nv_bfloat16* dst = p.o + static_cast<size_t>(warp_row) * p.ld + d.h * HD + 32 * (c - 1) + 8 * g;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int rr = 4 * k + (lane >> 3);
+              if (warp_row + rr < d.q1)
+                *reinterpret_cast<uint4*>(dst + static_cast<size_t>(rr) * p.ld) =
+                    *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
+            }
+          }
+        }
+        __syncwarp();
       }
     }
   }
@@ -477,7 +604,7 @@ template <int HD>
 __global__ void __launch_bounds__(256) k_cross_combine(const __grid_constant__ CrossParams p) {
   const int lane = threadIdx.x & 31;
   const int rr = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int unit = p.n_full + blockIdx.y;
+  const int unit = blockIdx.y;
   const int h = unit / p.units_per_head;
   int b, q0, q1;
   unit_rows(p, unit - h * p.units_per_head, b, q0, q1);
@@ -533,23 +660,40 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
   p.kv_mask = a.kv_mask;
   p.flag = c.flag;
   constexpr int smem = CrossCfg<HD>::kSmem;
-  static std::atomic<uint64_t> smem_set{0};  // per device
+  static std::atomic<uint64_t> smem_set[2] = {};  // per device
+  const bool mask = a.kv_mask != nullptr;
   {
-    const cudaError_t e = ensure_smem_limit(k_cross<HD>, smem, c.device, smem_set);
+    const cudaError_t e = mask ? ensure_smem_limit(k_cross<HD, true>, smem, c.device, smem_set[1])
+                               : ensure_smem_limit(k_cross<HD, false>, smem, c.device, smem_set[0]);
     if (e != cudaSuccess) return e;
   }
   p.units_per_head = a.n / kUnitQ + a.B;
   const int64_t units64 = static_cast<int64_t>(p.units_per_head) * H;
-  if (units64 > 0x3fffffff) {
+  if (units64 > 0x3fffffff / kMaxSplitParts) {
     if (why) *why = "too many sequences";
     return cudaErrorInvalidValue;
   }
-  const int units = static_cast<int>(units64);
-  p.n_full = units;
+  p.units = static_cast<int>(units64);
+  // Key ranges per unit: the rounds of CTAs times the tiles of a range, plus two
+  // tiles' time for a unit's own ends and six for the merge, whichever is least.
+  const int tiles = (a.S + kKV - 1) / kKV;
+  auto cost = [&](int sp) {
+    const int64_t rounds = (units64 * sp + c.num_sms - 1) / c.num_sms;
+    return rounds * ((tiles + sp - 1) / sp + 2) + (sp > 1 ? 6 : 0);
+  };
   p.split = 1;
+  for (int sp = 2; sp <= tiles && sp <= kMaxSplitParts && units64 * sp <= kMaxAttnParts; ++sp)
+    if (cost(sp) < cost(p.split)) p.split = sp;
   p.part_o = c.attn_part_o;
   p.part_ml = reinterpret_cast<float2*>(c.attn_part_ml);
-  k_cross<HD><<<units, kThreads, smem, c.stream>>>(tq, tk, tv, p);
+  const int64_t items = units64 * p.split;
+  const unsigned grid = static_cast<unsigned>(items < c.num_sms ? items : c.num_sms);
+  if (mask) k_cross<HD, true><<<grid, kThreads, smem, c.stream>>>(tq, tk, tv, p);
+  else k_cross<HD, false><<<grid, kThreads, smem, c.stream>>>(tq, tk, tv, p);
+  c.launches += 1;
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.split == 1) return e;
+  k_cross_combine<HD><<<dim3(kUnitQ / 8, p.units), 256, 0, c.stream>>>(p);
   c.launches += 1;
   return cudaGetLastError();
 }
