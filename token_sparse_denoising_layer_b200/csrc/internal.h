@@ -20,6 +20,7 @@ constexpr int kMaxQkSteps = 20;    // 512-place steps of a row the norm + rotati
 // Padded keys of a sequence: an empty mask of so many is looked through well
 // inside the time that a bounded wait allows.
 constexpr int kMaxCrossKeys = 1 << 26;
+constexpr int kVecRows = 4;  // rows up to which an 8-bit product streams its weights
 // Longest row of an 8-bit product: 128 * 128 * 131071 still fits 32-bit sums.
 constexpr int kMaxQuantK = 131071;
 constexpr int kMaxLnQuantD = 40 * 128;  // widest row of the LayerNorm that quantises
@@ -207,6 +208,9 @@ struct GemmArgs {
 cudaError_t launch_gemm(const Ctx& c, const GemmArgs& a, std::string* why);
 // The same product of signed 8-bit operands with scales (a.a_scale set).
 cudaError_t launch_gemm_s8(const Ctx& c, const GemmArgs& a, std::string* why);
+// The same with a plain store, where there are too few rows to fill the GPU with
+// launch_gemm_s8's tiles; *taken says whether that is so and it was launched.
+cudaError_t launch_linear_s8_few(const Ctx& c, const GemmArgs& a, bool* taken, std::string* why);
 
 // Attention of n queries against n_kv key/value rows (row stride D).
 cudaError_t launch_attention(const Ctx& c, const void* q, int n, const void* kc, const void* vc,

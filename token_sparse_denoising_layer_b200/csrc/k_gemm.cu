@@ -182,35 +182,37 @@ __device__ __forceinline__ void resid_chunk(const EpiParams& p, const uint32_t (
   __syncwarp();  // the stage is reused by the next chunk
 }
 
-// Integer sums of one chunk of a row -> fp32 products: float(sum) * sa * sb[j].
-// The integer sum is exact, so three roundings to 32 bits are all there are
-// before the epilogue's own.  Columns past Ncols are zero.
-__device__ __forceinline__ void dequant_chunk(const EpiParams& p, uint32_t (&r)[32], float sa,
-                                              int col) {
+// Scales of one chunk's columns (zero past Ncols).
+__device__ __forceinline__ void load_scales(const EpiParams& p, int col, F2 (&s)[16]) {
   if (col + 32 <= p.Ncols) {
     const float4* s4 = reinterpret_cast<const float4*>(p.b_scale + col);
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-      const float4 s = __ldg(s4 + v);
-      const F2 a = mul_x2(mul_x2(F2{__int2float_rn(static_cast<int>(r[4 * v])),
-                                    __int2float_rn(static_cast<int>(r[4 * v + 1]))},
-                                 splat(sa)),
-                          F2{s.x, s.y});
-      const F2 b = mul_x2(mul_x2(F2{__int2float_rn(static_cast<int>(r[4 * v + 2])),
-                                    __int2float_rn(static_cast<int>(r[4 * v + 3]))},
-                                 splat(sa)),
-                          F2{s.z, s.w});
-      r[4 * v] = __float_as_uint(a.x);
-      r[4 * v + 1] = __float_as_uint(a.y);
-      r[4 * v + 2] = __float_as_uint(b.x);
-      r[4 * v + 3] = __float_as_uint(b.y);
+      const float4 x = __ldg(s4 + v);
+      s[2 * v] = F2{x.x, x.y};
+      s[2 * v + 1] = F2{x.z, x.w};
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float s = col + e < p.Ncols ? __ldg(p.b_scale + col + e) : 0.f;
-      r[e] = __float_as_uint(__int2float_rn(static_cast<int>(r[e])) * sa * s);
-    }
+    for (int e = 0; e < 16; ++e)
+      s[e] = F2{col + 2 * e < p.Ncols ? __ldg(p.b_scale + col + 2 * e) : 0.f,
+                col + 2 * e + 1 < p.Ncols ? __ldg(p.b_scale + col + 2 * e + 1) : 0.f};
+  }
+}
+
+// Integer sums of one chunk of a row -> fp32 products: float(sum) * sa * sb[j].
+// The integer sum is exact, so three roundings to 32 bits are all there are
+// before the epilogue's own.
+__device__ __forceinline__ void dequant_chunk(uint32_t (&r)[32], float sa, const F2 (&s)[16]) {
+  const F2 sa2 = splat(sa);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const F2 x = mul_x2(mul_x2(F2{__int2float_rn(static_cast<int>(r[2 * e])),
+                                  __int2float_rn(static_cast<int>(r[2 * e + 1]))},
+                               sa2),
+                        s[e]);
+    r[2 * e] = __float_as_uint(x.x);
+    r[2 * e + 1] = __float_as_uint(x.y);
   }
 }
 
@@ -267,10 +269,11 @@ __device__ __forceinline__ void store_staged(const EpiParams& p, const uint8_t* 
 
 // Drain one accumulator tile: this warp's 32 rows (TMEM lanes at tbase),
 // output row m (this lane's), columns n0 .. n0 + kCols - 1.  TMEM loads run
-// one 32-column chunk ahead of the chunk being stored.
+// one 32-column chunk ahead of the chunk being stored.  `sa` is the row's scale
+// (8-bit operands).
 template <bool kS8, int kCols, int kEpi>
 __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, int m, int n0,
-                                           float* stage) {
+                                           float sa, float* stage) {
   constexpr int NC = kCols / 32;
   const bool mrow = m < p.M;
   int32_t dst_row = -1;
@@ -278,7 +281,6 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
     dst_row = __ldg(p.idx + m);
     if (!row_ok(dst_row, p.N, p.flag)) dst_row = -1;
   }
-  const float sa = kS8 && mrow ? __ldg(p.a_scale + m) : 0.f;
   uint32_t ra[32], rb[32];
   __syncwarp();
   tmem_ld32_nowait(tbase, ra);
@@ -286,6 +288,8 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
   for (int c = 0; c < NC; ++c) {
     uint32_t(&cur)[32] = (c & 1) ? rb : ra;
     uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
+    F2 sb[16];
+    if (kS8) load_scales(p, n0 + 32 * c, sb);  // on their way while TMEM is waited for
     tmem_wait_ld();
     if (c + 1 < NC) {
       __syncwarp();
@@ -293,7 +297,7 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
     }
     const int col = n0 + 32 * c;
     if (col >= p.Ncols) continue;  // uniform over the warp
-    if (kS8) dequant_chunk(p, cur, sa, col);
+    if (kS8) dequant_chunk(cur, sa, sb);
     if (kS8 && kEpi == EPI_STORE) {
       if ((p.ld_out & 7) != 0) {
         store_ragged(p, cur, m, col, stage);
@@ -340,13 +344,13 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
 }
 
 template <bool kS8, int kCols>
-__device__ __forceinline__ void drain(const EpiParams& p, uint32_t tbase, int m, int n0,
+__device__ __forceinline__ void drain(const EpiParams& p, uint32_t tbase, int m, int n0, float sa,
                                       float* stage) {
   switch (p.epi) {
-    case EPI_STORE: drain_tile<kS8, kCols, EPI_STORE>(p, tbase, m, n0, stage); break;
-    case EPI_GELU: drain_tile<kS8, kCols, EPI_GELU>(p, tbase, m, n0, stage); break;
-    case EPI_QKV: drain_tile<kS8, kCols, EPI_QKV>(p, tbase, m, n0, stage); break;
-    case EPI_RESID: drain_tile<kS8, kCols, EPI_RESID>(p, tbase, m, n0, stage); break;
+    case EPI_STORE: drain_tile<kS8, kCols, EPI_STORE>(p, tbase, m, n0, sa, stage); break;
+    case EPI_GELU: drain_tile<kS8, kCols, EPI_GELU>(p, tbase, m, n0, sa, stage); break;
+    case EPI_QKV: drain_tile<kS8, kCols, EPI_QKV>(p, tbase, m, n0, sa, stage); break;
+    case EPI_RESID: drain_tile<kS8, kCols, EPI_RESID>(p, tbase, m, n0, sa, stage); break;
     default: break;
   }
 }
@@ -473,15 +477,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int lt = 0;
     for (int t = blockIdx.x; t < total_tiles; t += gridDim.x, ++lt) {
       const int b = lt & 1;
+      const int m = (t / n_tiles) * kBM + row, n0 = (t % n_tiles) * BN + half * (BN / 2);
+      const float sa = kS8 && m < p.M ? __ldg(p.a_scale + m) : 0.f;
       if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[b], (lt >> 1) & 1))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const int m = (t / n_tiles) * kBM + row, n0 = (t % n_tiles) * BN + half * (BN / 2);
       const uint32_t tbase =
           tmem + b * BN + half * (BN / 2) + (static_cast<uint32_t>(32 * q) << 16);
-      drain<kS8, BN / 2>(p, tbase, m, n0, stage + (warp - 2) * kStageWarpFloats);
+      drain<kS8, BN / 2>(p, tbase, m, n0, sa, stage + (warp - 2) * kStageWarpFloats);
       // the buffer may be refilled once every lane's TMEM reads are done
       tc_fence_before();
       __syncwarp();
@@ -620,17 +625,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     int lt = 0;
     for (int t = pair; t < total_tiles; t += npairs, ++lt) {
       const int b = lt & 1;
+      const int m = (t / n_tiles) * 256 + rank * 128 + row, n0 = (t % n_tiles) * 256 + half * 128;
+      const float sa = kS8 && m < p.M ? __ldg(p.a_scale + m) : 0.f;
       if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[b], (lt >> 1) & 1))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const int m = (t / n_tiles) * 256 + rank * 128 + row, n0 = (t % n_tiles) * 256 + half * 128;
       const uint32_t tbase = tmem + b * 256 + half * 128 + (static_cast<uint32_t>(32 * q) << 16);
-      drain<kS8, 128>(p, tbase, m, n0, stage + (warp - 2) * kStageWarpFloats);
+      drain<kS8, 128>(p, tbase, m, n0, sa, stage + (warp - 2) * kStageWarpFloats);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(b == 0 ? lead_empty0 : lead_empty1);
+      if (lane == 0) {
+        if (kS8) mbar_arrive_cluster_tmem(b == 0 ? lead_empty0 : lead_empty1);
+        else mbar_arrive_cluster(b == 0 ? lead_empty0 : lead_empty1);
+      }
     }
   }
   if (!ok) atomicOr(p.flag, DEV_TIMEOUT);
@@ -770,6 +779,11 @@ cudaError_t launch_gemm(const Ctx& c, const GemmArgs& a, std::string* why) {
 
 cudaError_t launch_gemm_s8(const Ctx& c, const GemmArgs& a, std::string* why) {
   if (a.M <= 0) return cudaSuccess;
+  if (a.epi == EPI_STORE) {
+    bool taken = false;
+    const cudaError_t e = launch_linear_s8_few(c, a, &taken, why);
+    if (taken) return e;
+  }
   Timed timed(c, TC_GEMM, 2.0 * a.M * a.Ncols * a.Kd);
   // As above, by tile-waves x tile width; columns may end inside a tile.
   const int mt = (a.M + kBM - 1) / kBM;
