@@ -474,6 +474,9 @@ def _cross_case(seed, H, Hk, d, starts, S, lens, holes, n=None, q_scale=2.0):
     (1, 1, 128, [0, 2, 4, 300], 5000, [5000, 0, 1], 0),        # key ranges of a sequence without keys
     (2, 1, 64, [0, 5, 9], 3000, [2999, 200], 0.995),           # ranges without a seen key
     (12, 12, 128, [0, 3000, 6111], 300, [300, 129], 0),        # several units a CTA
+    (4, 4, 128, [0, 1, 2, 2, 3], 700, [700, 513, 9, 0], 0.3),  # single tokens, keys over a cluster
+    (4, 1, 64, [0, 2, 4], 5000, [4999, 1], 0),                 # two queries x four heads a key head
+    (12, 4, 128, [0] * 30 + [1, 20, 21], 130, [130 - b for b in range(32)], 0.1),  # one long one among short ones
     (4, 4, 64, [0, 8000, 8001, 20001], 333, [333, 333, 64], 0.2),
     (2, 2, 64, list(range(0, 4501, 3)), 40, [b % 41 for b in range(1500)], 0),  # more sequences than one search step
 ])

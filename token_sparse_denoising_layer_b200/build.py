@@ -23,7 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhsa.so")
 SOURCES = ["api.cu", "k_tokens.cu", "k_rows.cu", "k_gemm.cu", "k_attn.cu", "k_select_static.cu",
-           "k_rotary.cu", "k_quant.cu", "k_linear_s8.cu", "k_cross.cu"]
+           "k_rotary.cu", "k_quant.cu", "k_linear_s8.cu", "k_cross.cu",
+           "k_cross_few.cu"]
 HEADERS = ["ptx.cuh", "attn_tile.cuh", "internal.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

@@ -250,6 +250,9 @@ cudaError_t launch_ln_gather_quant(const Ctx& c, const float* x, const int32_t* 
 
 // Ragged cross-attention (see hsa_cross_attention).
 cudaError_t launch_cross_attention(const Ctx& c, const hsa_cross_args& a, std::string* why);
+// The same where sequences have a few queries each; *taken says whether they do
+// and it was launched.
+cudaError_t launch_cross_few(const Ctx& c, const hsa_cross_args& a, bool* taken);
 
 // TMA descriptor for a row-major matrix of bytes [rows, cols], rows ld bytes
 // apart, with a box of [box_rows, 128] and 128-byte swizzle.

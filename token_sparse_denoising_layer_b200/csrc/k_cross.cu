@@ -702,6 +702,9 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
 
 cudaError_t launch_cross_attention(const Ctx& c, const hsa_cross_args& a, std::string* why) {
   Timed timed(c, TC_ATTN, 4.0 * a.n * a.S * c.cfg.D);  // every key seen
+  bool taken = false;
+  const cudaError_t e = launch_cross_few(c, a, &taken);
+  if (taken) return e;
   return c.cfg.D / c.cfg.H == 128 ? launch_hd<128>(c, a, why) : launch_hd<64>(c, a, why);
 }
 

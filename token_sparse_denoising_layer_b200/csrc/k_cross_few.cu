@@ -1,0 +1,321 @@
+// k_cross_few.cu - cross-attention where sequences have a few queries each
+// (single tokens, guided pairs of them): hsa_cross_attention's result without
+// the 128-query tiles of k_cross.cu, which such sequences leave empty.
+//
+// Every key and value is read once for up to kFewRows rows that share it (the queries of
+// a sequence times the query heads of a key head), so what bounds this is HBM
+// and, before that, the bytes in flight.  A lane group of d / 8 lanes owns a
+// key: 16 bytes of K and of V a lane, kBatch keys loaded together.  Scores are
+// summed over the group by shuffles; each group keeps its own running maximum,
+// sum and output in fp32 (weights are never rounded to 16 bits here), and these are
+// merged over the groups of a warp by shuffles, over the warps of a CTA in shared
+// memory and over the CTAs of a cluster, which split the keys when there are
+// few sequences, through distributed shared memory.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace hsa {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kBatch = 4;    // keys of a lane group loaded together
+constexpr int kFewRows = 4;  // rows of one pass over the keys
+
+struct FewParams {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* o;
+  int64_t ld_k, bs_k, ld_v, bs_v;
+  int ld;  // D
+  int n, B, S, kv_heads, group, split;
+  float scale_log2;
+  const int32_t *q_start, *kv_len;
+  const uint8_t* kv_mask;
+  int* flag;
+};
+
+__device__ __forceinline__ int clamped(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
+  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(r[i] << 16);
+    f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+  }
+}
+
+// Running softmax state of one row in one lane: maximum (log2 units), sum, and
+// this lane's 8 output places, all relative to the maximum.
+struct Run {
+  float m, l, o[8];
+  // Takes in another state of the same row (of other keys).
+  __device__ __forceinline__ void merge(float m2, float l2, const float (&o2)[8]) {
+    const float top = fmaxf(m, m2), a = ex2_approx(m - top), b = ex2_approx(m2 - top);
+    m = top;
+    l = l * a + l2 * b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * a + o2[i] * b;
+  }
+};
+
+template <int HD, int R>
+__global__ void __launch_bounds__(32 * kWarps) k_cross_few(const __grid_constant__ FewParams p) {
+  constexpr int L = HD / 8, G = 32 / L;  // lanes per key, keys per warp step
+  __shared__ float s_ml[kWarps][R][2];
+  __shared__ __align__(16) float s_o[kWarps][R][HD];
+  __shared__ float c_ml[R][2];
+  __shared__ __align__(16) float c_o[R][HD];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane / L, e = 8 * (lane % L);  // key of the warp's step, first place of this lane
+
+  if (blockIdx.x == 0) {  // one CTA looks the offsets and lengths over
+    for (int i = threadIdx.x; i < p.B; i += 32 * kWarps) {
+      const int a = p.q_start[i], z = p.q_start[i + 1];
+      const int len = p.kv_len != nullptr ? p.kv_len[i] : 0;
+      if (a < 0 || z > p.n || a > z || len < 0 || len > p.S) atomicOr(p.flag, DEV_BAD_INDEX);
+    }
+  }
+  const int rank = blockIdx.x % p.split;
+  const int item = blockIdx.x / p.split;
+  const int kvh = item % p.kv_heads, b = item / p.kv_heads;
+  const int q0 = clamped(__ldg(p.q_start + b), 0, p.n);
+  const int q1 = clamped(__ldg(p.q_start + b + 1), 0, p.n);
+  if (q0 >= q1) return;  // the same for every CTA of the cluster
+  const int len = p.kv_len != nullptr ? clamped(__ldg(p.kv_len + b), 0, p.S) : p.S;
+  const int rows = (q1 - q0) * p.group;
+  const __nv_bfloat16* kb = p.k + b * p.bs_k + kvh * HD + e;
+  const __nv_bfloat16* vb = p.v + b * p.bs_v + kvh * HD + e;
+  const uint8_t* mask = p.kv_mask == nullptr ? nullptr : p.kv_mask + static_cast<int64_t>(b) * p.S;
+  // this CTA's keys, a multiple of a warp's batch
+  const int per = ((len + p.split - 1) / p.split + G * kBatch - 1) / (G * kBatch) * (G * kBatch);
+  const int first = min(len, rank * per), last = min(len, first + per);
+
+  for (int r0 = 0; r0 < rows; r0 += R) {
+    float qf[R][8];
+    Run run[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int rr = min(r0 + r, rows - 1);
+      const int head = kvh * p.group + rr % p.group;
+      unpack8(__ldg(reinterpret_cast<const uint4*>(
+                  p.q + static_cast<int64_t>(q0 + rr / p.group) * p.ld + head * HD + e)),
+              qf[r]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qf[r][i] *= p.scale_log2, run[r].o[i] = 0.f;
+      run[r].m = -FLT_MAX;
+      run[r].l = 0.f;
+    }
+    for (int j0 = first + warp * G * kBatch; j0 < last; j0 += kWarps * G * kBatch) {
+      uint4 kr[kBatch], vr[kBatch];
+      bool see[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int j = j0 + u * G + g;
+        see[u] = j < last;
+        kr[u] = vr[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (see[u]) {
+          kr[u] = __ldg(reinterpret_cast<const uint4*>(kb + j * p.ld_k));
+          vr[u] = __ldg(reinterpret_cast<const uint4*>(vb + j * p.ld_v));
+          if (mask != nullptr) see[u] = __ldg(mask + j) != 0;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)  // a weight of 0 would not silence a NaN
+        if (!see[u]) vr[u] = make_uint4(0u, 0u, 0u, 0u);
+      float s[R][kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        float kf[8];
+        unpack8(kr[u], kf);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float d = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d = fmaf(qf[r][i], kf[i], d);
+          s[r][u] = d;
+        }
+      }
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) s[r][u] += __shfl_xor_sync(0xffffffffu, s[r][u], o);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float top = run[r].m;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (!see[u]) s[r][u] = -INFINITY;
+          top = fmaxf(top, s[r][u]);
+        }
+        const float keep = ex2_approx(run[r].m - top);
+        run[r].m = top;
+        run[r].l *= keep;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) run[r].o[i] *= keep;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          s[r][u] = ex2_approx(s[r][u] - top);
+          run[r].l += s[r][u];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        float vf[8];
+        unpack8(vr[u], vf);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) run[r].o[i] = fmaf(s[r][u], vf[i], run[r].o[i]);
+      }
+    }
+    // the lane groups of the warp
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float o2[8];
+        const float m2 = __shfl_xor_sync(0xffffffffu, run[r].m, o);
+        const float l2 = __shfl_xor_sync(0xffffffffu, run[r].l, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o2[i] = __shfl_xor_sync(0xffffffffu, run[r].o[i], o);
+        run[r].merge(m2, l2, o2);
+      }
+    // the warps of the CTA
+    if (g == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (e == 0) s_ml[warp][r][0] = run[r].m, s_ml[warp][r][1] = run[r].l;
+        float4* dst = reinterpret_cast<float4*>(&s_o[warp][r][e]);
+        dst[0] = make_float4(run[r].o[0], run[r].o[1], run[r].o[2], run[r].o[3]);
+        dst[1] = make_float4(run[r].o[4], run[r].o[5], run[r].o[6], run[r].o[7]);
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < R * HD; i += 32 * kWarps) {
+      const int r = i / HD, c = i % HD;
+      float top = -FLT_MAX;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r][0]);
+      float l = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2_approx(s_ml[w][r][0] - top);
+        l = fmaf(s_ml[w][r][1], f, l);
+        o = fmaf(s_o[w][r][c], f, o);
+      }
+      if (p.split == 1) {
+        if (r0 + r < rows) {
+          const int rr = r0 + r, head = kvh * p.group + rr % p.group;
+          p.o[static_cast<int64_t>(q0 + rr / p.group) * p.ld + head * HD + c] =
+              __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+        }
+      } else {
+        c_o[r][c] = o;
+        if (c == 0) c_ml[r][0] = top, c_ml[r][1] = l;
+      }
+    }
+    if (p.split == 1) {
+      __syncthreads();  // the next rows reuse the shared memory
+      continue;
+    }
+    cluster_sync();
+    // the CTAs of the cluster: rank k writes the places c with c % split == k
+    for (int i = threadIdx.x; i < R * (HD / p.split); i += 32 * kWarps) {
+      const int r = i / (HD / p.split), c = i % (HD / p.split) * p.split + rank;
+      float m[8], l[8], o[8];
+      float top = -FLT_MAX;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k >= p.split) break;
+        m[k] = ld_cluster_f32(&c_ml[r][0], k);
+        l[k] = ld_cluster_f32(&c_ml[r][1], k);
+        o[k] = ld_cluster_f32(&c_o[r][c], k);
+        top = fmaxf(top, m[k]);
+      }
+      float ls = 0.f, os = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k >= p.split) break;
+        const float f = ex2_approx(m[k] - top);
+        ls = fmaf(l[k], f, ls);
+        os = fmaf(o[k], f, os);
+      }
+      if (r0 + r < rows) {
+        const int rr = r0 + r, head = kvh * p.group + rr % p.group;
+        p.o[static_cast<int64_t>(q0 + rr / p.group) * p.ld + head * HD + c] =
+            __float2bfloat16_rn(ls == 0.f ? 0.f : os / ls);
+      }
+    }
+    cluster_sync();  // no CTA reuses or leaves its state while another may read it
+  }
+}
+
+template <int HD, int R>
+cudaError_t launch_rows(const Ctx& c, const FewParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.kv_heads * p.split);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_cross_few<HD, R>, p);
+  c.launches += 1;
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_few(const Ctx& c, const hsa_cross_args& a, bool* taken) {
+  const int H = c.cfg.H, hd = c.cfg.D / H, group = H / a.kv_heads;
+  const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads;
+  // Up to two passes over the keys for a sequence of average length; longer ones
+  // are worth a 128-query tile.
+  *taken = static_cast<int64_t>(a.n) * group <= static_cast<int64_t>(a.B) * 2 * kFewRows &&
+           items * 8 < 0x7fffffff;
+  if (!*taken) return cudaSuccess;
+  FewParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k = static_cast<const __nv_bfloat16*>(a.k);
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.ld_k = a.ld_k;
+  p.bs_k = a.bs_k;
+  p.ld_v = a.ld_v;
+  p.bs_v = a.bs_v;
+  p.ld = c.cfg.D;
+  p.n = a.n;
+  p.B = a.B;
+  p.S = a.S;
+  p.kv_heads = a.kv_heads;
+  p.group = group;
+  const double scale = a.scale != 0.f ? a.scale : 1.0 / sqrt(static_cast<double>(hd));
+  p.scale_log2 = static_cast<float>(1.4426950408889634 * scale);
+  p.q_start = a.q_start;
+  p.kv_len = a.kv_len;
+  p.kv_mask = a.kv_mask;
+  p.flag = c.flag;
+  // Keys over a cluster while there are fewer than two CTAs an SM and each
+  // keeps a batch for every warp.
+  const int batch = kWarps * kBatch * (256 / hd);
+  p.split = 1;
+  while (p.split < 8 && items * p.split < 2 * c.num_sms && a.S >= 2 * p.split * batch) p.split *= 2;
+  const bool one = static_cast<int64_t>(a.n) * group <= a.B;  // a single row per sequence
+  if (hd == 128) return one ? launch_rows<128, 1>(c, p) : launch_rows<128, kFewRows>(c, p);
+  return one ? launch_rows<64, 1>(c, p) : launch_rows<64, kFewRows>(c, p);
+}
+
+}  // namespace hsa
