@@ -575,12 +575,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             // one store covers four rows and 128 contiguous bytes of each
             __syncwarp();
             __nv_bfloat16* dst = p.o + static_cast<size_t>(warp_row) * p.ld + d.h * HD + 32 * (c - 1) + 8 * g;
+            uint4 w[8];  // read all before the first is stored: a load waits behind a store
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int rr = 4 * k + (lane >> 3);
-              if (warp_row + rr < d.q1)
-                *reinterpret_cast<uint4*>(dst + static_cast<size_t>(rr) * p.ld) =
-                    *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
+              w[k] = *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int rr = 4 * k + (lane >> 3);
+              if (warp_row + rr < d.q1) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(rr) * p.ld) = w[k];
             }
           }
         }

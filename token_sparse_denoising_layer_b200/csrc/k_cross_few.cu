@@ -67,7 +67,7 @@ struct Run {
 };
 
 template <int HD, int R>
-__global__ void __launch_bounds__(32 * kWarps) k_cross_few(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(32 * kWarps, R == 1 ? 3 : R == 2 ? 2 : 1) k_cross_few(const __grid_constant__ FewParams p) {
   constexpr int L = HD / 8, G = 32 / L;  // lanes per key, keys per warp step
   __shared__ float s_ml[kWarps][R][2];
   __shared__ __align__(16) float s_o[kWarps][R][HD];
@@ -282,10 +282,11 @@ cudaError_t launch_rows(const Ctx& c, const FewParams& p) {
 cudaError_t launch_cross_few(const Ctx& c, const hsa_cross_args& a, bool* taken) {
   const int H = c.cfg.H, hd = c.cfg.D / H, group = H / a.kv_heads;
   const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads;
-  // Up to two passes over the keys for a sequence of average length; longer ones
-  // are worth a 128-query tile.
-  *taken = static_cast<int64_t>(a.n) * group <= static_cast<int64_t>(a.B) * 2 * kFewRows &&
-           items * 8 < 0x7fffffff;
+  // One pass over the keys for a sequence of average length.  With more rows a
+  // 128-query tile is faster although most of it is empty (16 sequences, 512 keys: 4 rows
+  // a key head 25 us here and 40 in tiles, 6 rows 55 and 23).
+  const int64_t rows = static_cast<int64_t>(a.n) * group;
+  *taken = rows <= static_cast<int64_t>(a.B) * kFewRows && items * 8 < 0x7fffffff;
   if (!*taken) return cudaSuccess;
   FewParams p{};
   p.q = static_cast<const __nv_bfloat16*>(a.q);
@@ -313,9 +314,10 @@ cudaError_t launch_cross_few(const Ctx& c, const hsa_cross_args& a, bool* taken)
   const int batch = kWarps * kBatch * (256 / hd);
   p.split = 1;
   while (p.split < 8 && items * p.split < 2 * c.num_sms && a.S >= 2 * p.split * batch) p.split *= 2;
-  const bool one = static_cast<int64_t>(a.n) * group <= a.B;  // a single row per sequence
-  if (hd == 128) return one ? launch_rows<128, 1>(c, p) : launch_rows<128, kFewRows>(c, p);
-  return one ? launch_rows<64, 1>(c, p) : launch_rows<64, kFewRows>(c, p);
+  const int r = rows <= a.B ? 1 : rows <= 2 * static_cast<int64_t>(a.B) ? 2 : kFewRows;
+  if (hd == 128)
+    return r == 1 ? launch_rows<128, 1>(c, p) : r == 2 ? launch_rows<128, 2>(c, p) : launch_rows<128, kFewRows>(c, p);
+  return r == 1 ? launch_rows<64, 1>(c, p) : r == 2 ? launch_rows<64, 2>(c, p) : launch_rows<64, kFewRows>(c, p);
 }
 
 }  // namespace hsa

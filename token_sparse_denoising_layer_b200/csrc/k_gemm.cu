@@ -255,13 +255,18 @@ __device__ __forceinline__ void store_staged(const EpiParams& p, const uint8_t* 
   const int lane = threadIdx.x & 31;
   const int g = lane & 7;
   __syncwarp();
+  uint4 w[8];  // read all before the first is stored: a load waits behind a store
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int rr = 4 * k + (lane >> 3);
+    w[k] = *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
+  }
   if (col + 8 * g < end) {
+    __nv_bfloat16* dst = p.out + static_cast<size_t>(m0) * p.ld_out + col + 8 * g;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int rr = 4 * k + (lane >> 3);
-      if (m0 + rr < p.M)
-        *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(m0 + rr) * p.ld_out + col + 8 * g) =
-            *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
+      if (m0 + rr < p.M) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(rr) * p.ld_out) = w[k];
     }
   }
   __syncwarp();  // the stage is reused by the next 64 columns
