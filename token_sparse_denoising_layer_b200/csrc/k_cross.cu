@@ -167,7 +167,8 @@ __device__ __forceinline__ void hide(uint32_t (&sr)[kKV], const uint32_t (&w)[4]
 template <int HD, bool kMask>
 __global__ void __launch_bounds__(kThreads, 1)
     k_cross(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CrossParams p) {
+            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+            const __grid_constant__ CrossParams p) {
   using Cfg = CrossCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -563,6 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t r[32];
           __syncwarp();
           tmem_ld32(tO + 32 * c, r);
+          if (!(c & 1)) {  // the stage may still be on its way out
+            if (lane == 0) tma_store_wait_read();
+            __syncwarp();
+          }
           // this lane's row of the stage: 64 columns, 16-byte group v at v ^ (row & 7)
 #pragma unroll
           for (int v = 0; v < 4; ++v)
@@ -571,26 +576,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pack_bf16(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv),
                 pack_bf16(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv),
                 pack_bf16(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv));
-          if (c & 1) {
-            // one store covers four rows and 128 contiguous bytes of each
+          if (!(c & 1)) continue;
+          if (warp_row + 32 <= d.q1) {
+            // 32 rows of this sequence: one tiled store, which this warp does not
+            // wait for (an SM stores about 32 bytes a clock: 2000 clocks a unit)
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmO, stage, d.h * HD + 32 * (c - 1), warp_row);
+              tma_store_commit();
+            }
+          } else {
+            // the next rows are another sequence's: one store covers four rows
+            // and 128 contiguous bytes of each
             __syncwarp();
             __nv_bfloat16* dst = p.o + static_cast<size_t>(warp_row) * p.ld + d.h * HD + 32 * (c - 1) + 8 * g;
-            uint4 w[8];  // read all before the first is stored: a load waits behind a store
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int rr = 4 * k + (lane >> 3);
-              w[k] = *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
+              if (warp_row + rr < d.q1)
+                *reinterpret_cast<uint4*>(dst + static_cast<size_t>(rr) * p.ld) =
+                    *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
             }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int rr = 4 * k + (lane >> 3);
-              if (warp_row + rr < d.q1) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(rr) * p.ld) = w[k];
-            }
+            __syncwarp();
           }
         }
-        __syncwarp();
       }
     }
+    if (lane == 0) tma_store_wait();  // also keeps the stage until it is read
   }
   if (!ok) atomicOr(p.flag, DEV_TIMEOUT);
   tc_fence_before();
@@ -642,12 +655,13 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
   const int D = c.cfg.D, H = c.cfg.H;
   const bool k1 = a.B == 1 || a.bs_k == 0, v1 = a.B == 1 || a.bs_v == 0;
   const uint64_t width = static_cast<uint64_t>(a.kv_heads) * HD;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   if (!make_tmap_bf16(&tq, a.q, a.n, D, D, kQ, why)) return cudaErrorInvalidValue;
   if (!make_tmap_bf16_3d(&tk, a.k, k1 ? 1 : a.B, a.S, width, a.ld_k, k1 ? a.ld_k * a.S : a.bs_k, kKV, why))
     return cudaErrorInvalidValue;
   if (!make_tmap_bf16_3d(&tv, a.v, v1 ? 1 : a.B, a.S, width, a.ld_v, v1 ? a.ld_v * a.S : a.bs_v, kKV, why))
     return cudaErrorInvalidValue;
+  if (!make_tmap_bf16(&to, a.o, a.n, D, D, 32, why)) return cudaErrorInvalidValue;
   CrossParams p{};
   p.n = a.n;
   p.B = a.B;
@@ -692,8 +706,8 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
   p.part_ml = reinterpret_cast<float2*>(c.attn_part_ml);
   const int64_t items = units64 * p.split;
   const unsigned grid = static_cast<unsigned>(items < c.num_sms ? items : c.num_sms);
-  if (mask) k_cross<HD, true><<<grid, kThreads, smem, c.stream>>>(tq, tk, tv, p);
-  else k_cross<HD, false><<<grid, kThreads, smem, c.stream>>>(tq, tk, tv, p);
+  if (mask) k_cross<HD, true><<<grid, kThreads, smem, c.stream>>>(tq, tk, tv, to, p);
+  else k_cross<HD, false><<<grid, kThreads, smem, c.stream>>>(tq, tk, tv, to, p);
   c.launches += 1;
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.split == 1) return e;
