@@ -247,29 +247,39 @@ __device__ __forceinline__ void stage_half(uint8_t* stage, const uint32_t (&r)[3
     *reinterpret_cast<uint4*>(stage + lane * 128 + 16 * ((4 * half + v) ^ (lane & 7))) = w[v];
 }
 
-// Store the warp's staged rows, up to 64 columns of them from `col` on: one
-// instruction covers four rows and 128 contiguous bytes of each, where a store
-// straight from a lane's own row would touch 32 rows and half a sector of each.
-__device__ __forceinline__ void store_staged(const EpiParams& p, const uint8_t* stage, int m0,
-                                             int col, int end) {
-  const int lane = threadIdx.x & 31;
-  const int g = lane & 7;
+// Send the warp's staged rows off, 64 columns of them from `col` on, as one tiled
+// store that clips what lies past M or Ncols.  The warp does not wait for it:
+// an SM stores about 32 bytes a clock, so a 128 x 256 tile's rows take 2000 clocks.
+__device__ __forceinline__ void store_staged(const CUtensorMap* tm_out, const uint8_t* stage,
+                                             int m0, int col) {
+  fence_proxy_async_smem();
   __syncwarp();
-  uint4 w[8];  // read all before the first is stored: a load waits behind a store
+  if ((threadIdx.x & 31) == 0) {
+    tma_store_2d(tm_out, stage, col, m0);
+    tma_store_commit();
+  }
+}
+
+// Store 32 staged columns (the first half of the stage's rows) where no second
+// half follows: one instruction covers eight rows and 64 bytes of each.
+__device__ __forceinline__ void store_half(const EpiParams& p, const uint8_t* stage, int m0, int col) {
+  const int lane = threadIdx.x & 31, g = lane & 3;
+  __syncwarp();
+  uint4 w[4];  // read all before the first is stored: a load waits behind a store
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int rr = 4 * k + (lane >> 3);
+  for (int k = 0; k < 4; ++k) {
+    const int rr = 8 * k + (lane >> 2);
     w[k] = *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
   }
-  if (col + 8 * g < end) {
-    __nv_bfloat16* dst = p.out + static_cast<size_t>(m0) * p.ld_out + col + 8 * g;
+  if (col + 8 * g < p.Ncols) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int rr = 4 * k + (lane >> 3);
-      if (m0 + rr < p.M) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(rr) * p.ld_out) = w[k];
+    for (int k = 0; k < 4; ++k) {
+      const int rr = 8 * k + (lane >> 2);
+      if (m0 + rr < p.M)
+        *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(m0 + rr) * p.ld_out + col + 8 * g) = w[k];
     }
   }
-  __syncwarp();  // the stage is reused by the next 64 columns
+  __syncwarp();  // the stage is reused by the next tile
 }
 
 // Drain one accumulator tile: this warp's 32 rows (TMEM lanes at tbase),
@@ -277,8 +287,8 @@ __device__ __forceinline__ void store_staged(const EpiParams& p, const uint8_t* 
 // one 32-column chunk ahead of the chunk being stored.  `sa` is the row's scale
 // (8-bit operands).
 template <bool kS8, int kCols, int kEpi>
-__device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, int m, int n0,
-                                           float sa, float* stage) {
+__device__ __forceinline__ void drain_tile(const EpiParams& p, const CUtensorMap* tm_out,
+                                           uint32_t tbase, int m, int n0, float sa, float* stage) {
   constexpr int NC = kCols / 32;
   const bool mrow = m < p.M;
   int32_t dst_row = -1;
@@ -308,10 +318,14 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
         store_ragged(p, cur, m, col, stage);
       } else {
         uint8_t* bytes = reinterpret_cast<uint8_t*>(stage);
+        if (!(c & 1)) {  // the stage may still be on its way out
+          if ((threadIdx.x & 31) == 0) tma_store_wait_read();
+          __syncwarp();
+        }
         stage_half(bytes, cur, c & 1);
-        if ((c & 1) || c + 1 == NC || col + 32 >= p.Ncols)
-          store_staged(p, bytes, m - (threadIdx.x & 31), col - 32 * (c & 1),
-                       min(p.Ncols, col + 32));
+        const int m0 = m - (threadIdx.x & 31);
+        if (c & 1) store_staged(tm_out, bytes, m0, col - 32);
+        else if (c + 1 == NC || col + 32 >= p.Ncols) store_half(p, bytes, m0, col);
       }
     } else if (kEpi == EPI_RESID) {
       resid_chunk(p, cur, dst_row, col, stage);
@@ -349,13 +363,13 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, uint32_t tbase, i
 }
 
 template <bool kS8, int kCols>
-__device__ __forceinline__ void drain(const EpiParams& p, uint32_t tbase, int m, int n0, float sa,
-                                      float* stage) {
+__device__ __forceinline__ void drain(const EpiParams& p, const CUtensorMap* tm_out, uint32_t tbase,
+                                      int m, int n0, float sa, float* stage) {
   switch (p.epi) {
-    case EPI_STORE: drain_tile<kS8, kCols, EPI_STORE>(p, tbase, m, n0, sa, stage); break;
-    case EPI_GELU: drain_tile<kS8, kCols, EPI_GELU>(p, tbase, m, n0, sa, stage); break;
-    case EPI_QKV: drain_tile<kS8, kCols, EPI_QKV>(p, tbase, m, n0, sa, stage); break;
-    case EPI_RESID: drain_tile<kS8, kCols, EPI_RESID>(p, tbase, m, n0, sa, stage); break;
+    case EPI_STORE: drain_tile<kS8, kCols, EPI_STORE>(p, tm_out, tbase, m, n0, sa, stage); break;
+    case EPI_GELU: drain_tile<kS8, kCols, EPI_GELU>(p, tm_out, tbase, m, n0, sa, stage); break;
+    case EPI_QKV: drain_tile<kS8, kCols, EPI_QKV>(p, tm_out, tbase, m, n0, sa, stage); break;
+    case EPI_RESID: drain_tile<kS8, kCols, EPI_RESID>(p, tm_out, tbase, m, n0, sa, stage); break;
     default: break;
   }
 }
@@ -372,7 +386,7 @@ __host__ __device__ constexpr int k_block() {
 template <bool kS8, int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-           EpiParams p, int n_tiles, int total_tiles) {
+           const __grid_constant__ CUtensorMap tmO, EpiParams p, int n_tiles, int total_tiles) {
   using Cfg = GemmCfg<BN>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -380,12 +394,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + S * Cfg::kABytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + S * Cfg::kBBytes);
+  float* stage = reinterpret_cast<float*>(sB + S * Cfg::kBBytes);  // 1024-byte aligned
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + S * Cfg::kBBytes + kEpiStageBytes);
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;     // [2] accumulator buffer ready for the epilogue
   uint64_t* acc_empty = acc_full + 2; // [2] accumulator buffer drained
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
-  float* stage = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + Cfg::kBarBytes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kKB = k_block<kS8>();
@@ -491,12 +505,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       const uint32_t tbase =
           tmem + b * BN + half * (BN / 2) + (static_cast<uint32_t>(32 * q) << 16);
-      drain<kS8, BN / 2>(p, tbase, m, n0, sa, stage + (warp - 2) * kStageWarpFloats);
+      drain<kS8, BN / 2>(p, &tmO, tbase, m, n0, sa, stage + (warp - 2) * kStageWarpFloats);
       // the buffer may be refilled once every lane's TMEM reads are done
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[b]);
     }
+    if (kS8 && lane == 0) tma_store_wait();  // rows in flight read this CTA's shared memory
   }
   if (!ok) atomicOr(p.flag, DEV_TIMEOUT);
   tc_fence_before();
@@ -524,19 +539,19 @@ constexpr int kPairSmem = kPairStages * kPairStageBytes + 256 + kEpiStageBytes +
 template <bool kS8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                EpiParams p, int n_tiles, int total_tiles) {
+                const __grid_constant__ CUtensorMap tmO, EpiParams p, int n_tiles, int total_tiles) {
   constexpr int S = kPairStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + S * kPairABytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + S * kPairBBytes);  // used in rank 0
+  float* stage = reinterpret_cast<float*>(sB + S * kPairBBytes);  // 1024-byte aligned
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + S * kPairBBytes + kEpiStageBytes);  // used in rank 0
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;      // [2]
   uint64_t* acc_empty = acc_full + 2;  // [2], used in rank 0
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
-  float* stage = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 256);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -638,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       }
       tc_fence_after();
       const uint32_t tbase = tmem + b * 256 + half * 128 + (static_cast<uint32_t>(32 * q) << 16);
-      drain<kS8, 128>(p, tbase, m, n0, sa, stage + (warp - 2) * kStageWarpFloats);
+      drain<kS8, 128>(p, &tmO, tbase, m, n0, sa, stage + (warp - 2) * kStageWarpFloats);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -646,6 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         else mbar_arrive_cluster(b == 0 ? lead_empty0 : lead_empty1);
       }
     }
+    if (kS8 && lane == 0) tma_store_wait();  // rows in flight read this CTA's shared memory
   }
   if (!ok) atomicOr(p.flag, DEV_TIMEOUT);
   tc_fence_before();
@@ -696,21 +712,29 @@ EpiParams epi_params(const Ctx& c, const GemmArgs& a) {
   return p;
 }
 
-// Operand maps with boxes of box_a and box_b rows of one K-block.
+// Operand maps with boxes of box_a and box_b rows of one K-block, and for 8-bit
+// operands the map of an aligned plain output (else unused).
 template <bool kS8>
 bool operand_maps(const GemmArgs& a, uint32_t box_a, uint32_t box_b, CUtensorMap* ta,
-                  CUtensorMap* tb, std::string* why) {
-  if (kS8)
-    return make_tmap_s8(ta, a.A, a.M, a.Kd, a.ld_a, box_a, why) &&
-           make_tmap_s8(tb, a.B, a.Ncols, a.Kd, a.ld_b, box_b, why);
-  return make_tmap_bf16(ta, a.A, a.M, a.Kd, a.Kd, box_a, why) &&
-         make_tmap_bf16(tb, a.B, a.Ncols, a.Kd, a.Kd, box_b, why);
+                  CUtensorMap* tb, CUtensorMap* to, std::string* why) {
+  if (kS8) {
+    if (!make_tmap_s8(ta, a.A, a.M, a.Kd, a.ld_a, box_a, why) ||
+        !make_tmap_s8(tb, a.B, a.Ncols, a.Kd, a.ld_b, box_b, why))
+      return false;
+    *to = *ta;
+    return a.epi != EPI_STORE || a.ld_out % 8 != 0 ||
+           make_tmap_bf16(to, a.out, a.M, a.Ncols, a.ld_out, 32, why);
+  }
+  const bool made = make_tmap_bf16(ta, a.A, a.M, a.Kd, a.Kd, box_a, why) &&
+                    make_tmap_bf16(tb, a.B, a.Ncols, a.Kd, a.Kd, box_b, why);
+  *to = *ta;
+  return made;
 }
 
 template <bool kS8>
 cudaError_t launch_pair(const Ctx& c, const GemmArgs& a, std::string* why) {
-  CUtensorMap ta, tb;
-  if (!operand_maps<kS8>(a, 128, 128, &ta, &tb, why)) return cudaErrorInvalidValue;
+  CUtensorMap ta, tb, to;
+  if (!operand_maps<kS8>(a, 128, 128, &ta, &tb, &to, why)) return cudaErrorInvalidValue;
   const EpiParams p = epi_params(c, a);
   static std::atomic<uint64_t> smem_set{0};  // per device
   {
@@ -720,15 +744,15 @@ cudaError_t launch_pair(const Ctx& c, const GemmArgs& a, std::string* why) {
   const int n_tiles = (a.Ncols + 255) / 256;
   const int total = n_tiles * ((a.M + 255) / 256);
   const int pairs = total < c.num_sms / 2 ? total : c.num_sms / 2;
-  k_gemm_pair<kS8><<<2 * pairs, kGemmThreads, kPairSmem, c.stream>>>(ta, tb, p, n_tiles, total);
+  k_gemm_pair<kS8><<<2 * pairs, kGemmThreads, kPairSmem, c.stream>>>(ta, tb, to, p, n_tiles, total);
   c.launches += 1;
   return cudaGetLastError();
 }
 
 template <bool kS8, int BN>
 cudaError_t launch_bn(const Ctx& c, const GemmArgs& a, std::string* why) {
-  CUtensorMap ta, tb;
-  if (!operand_maps<kS8>(a, kBM, BN, &ta, &tb, why)) return cudaErrorInvalidValue;
+  CUtensorMap ta, tb, to;
+  if (!operand_maps<kS8>(a, kBM, BN, &ta, &tb, &to, why)) return cudaErrorInvalidValue;
   const EpiParams p = epi_params(c, a);
   constexpr int smem = GemmCfg<BN>::kSmem;
   static std::atomic<uint64_t> smem_set{0};  // per device
@@ -739,7 +763,7 @@ cudaError_t launch_bn(const Ctx& c, const GemmArgs& a, std::string* why) {
   const int n_tiles = (a.Ncols + BN - 1) / BN;
   const int total = n_tiles * ((a.M + kBM - 1) / kBM);
   const int grid = total < c.num_sms ? total : c.num_sms;
-  k_gemm<kS8, BN><<<grid, kGemmThreads, smem, c.stream>>>(ta, tb, p, n_tiles, total);
+  k_gemm<kS8, BN><<<grid, kGemmThreads, smem, c.stream>>>(ta, tb, to, p, n_tiles, total);
   c.launches += 1;
   return cudaGetLastError();
 }
