@@ -588,7 +588,7 @@ hsa_status hsa_qk_norm_rope(hsa_ctx* ctx, const hsa_qk_rope* a, const int32_t* i
 typedef struct {
   const void* q;           /* (device) bf16 [n, D]: the sequences' queries one after another */
   const int32_t* q_start;  /* (device) int32 [B + 1], ascending, in [0, n]: sequence b owns rows
-                              q_start[b] .. q_start[b + 1] - 1 */
+                              q_start[b] .. q_start[b + 1] - 1; NULL: n / B rows each, n % B == 0 */
   int n, B;                /* n >= 0, B >= 1 */
   const void* k;           /* (device) bf16 [B, S, kv_heads * D/H], rows ld_k apart, */
   const void* v;           /*   sequences bs_k apart (elements); v likewise */
@@ -611,6 +611,48 @@ typedef struct {
  * that descends or leaves [0, n] is clamped; both are reported by hsa_sync_check.
  */
 hsa_status hsa_cross_attention(hsa_ctx* ctx, const hsa_cross_args* a);
+
+/* One transformer block's weights in signed 8 bits, as hsa_quant_rows makes them
+ * from the bf16 weights (a row per output channel, rows dense), with their scales. */
+typedef struct {
+  const int8_t *w_qkv, *w_o, *w_1, *w_2;         /* (device) int8 [3D, D], [D, D], [F, D], [D, F] */
+  const float *s_qkv, *s_o, *s_1, *s_2;          /* (device) fp32 [3D], [D], [F], [D] */
+} hsa_layer_weights_quant;
+
+/* What a block may have beyond hsa_layer_forward; zero-initialise and set what is wanted. */
+typedef struct {
+  const float* mod;                  /* as hsa_layer_forward_cond */
+  const hsa_cross_attn* xa;          /* as hsa_layer_forward_cond (weights in bf16) */
+  const int32_t* txt_len;            /* (device) int32 [1]: text tokens that count, in [0, n_txt]; NULL: n_txt */
+  const uint8_t* txt_mask;           /* (device) uint8 [n_txt], 0 = not seen; NULL: all seen */
+  const hsa_qk_rope* qk;             /* norm and rotation of the self-attention's Q and K; a token's
+                                        table row is its place in the latent */
+  const hsa_layer_weights_quant* wq; /* the four products in 8 bits; NULL: bf16 weights w */
+} hsa_block_ext;
+
+/*
+ * hsa_layer_forward_cond with the operators above inside the block:
+ *  - qk: Q and the fresh K rows are normalised and rotated (hsa_qk_norm_rope, in
+ *    place) between the QKV product and the attention, so the cache holds rotated keys;
+ *  - txt_len / txt_mask: the text cross-attention is hsa_cross_attention over the tokens
+ *    that count, read on the device: a captured step serves prompts of any length up to n_txt;
+ *  - wq: LN rows, attention output and MLP hidden rows are quantised per token
+ *    (hsa_ln_gather_quant, hsa_quant_rows) and multiplied in 8 bits; w is not read and may be NULL.
+ * ext == NULL or all members NULL is hsa_layer_forward.  Errors as
+ * hsa_layer_forward_cond and the calls named; with wq also HSA_ERR_SHAPE for
+ * D > 5120 or F > 36864.
+ */
+hsa_status hsa_layer_forward_ext(hsa_ctx* ctx, const hsa_layer_weights* w, const hsa_block_ext* ext,
+                                 float* x, const int32_t* idx, int n, void* k_cache, void* v_cache);
+
+/*
+ * hsa_step with every layer run by hsa_layer_forward_ext: ext is a host array of L
+ * entries, read during the call only, or NULL.  w->layers may be NULL when every
+ * entry has wq.
+ */
+hsa_status hsa_step_ext(hsa_ctx* ctx, const hsa_model_weights* w, const hsa_state* s,
+                        const hsa_block_ext* ext, int i, float sigma_i, float sigma_next,
+                        int regroup);
 
 /*
  * Group selection without any device allocation.  The paper has no

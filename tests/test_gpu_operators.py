@@ -538,6 +538,13 @@ def test_cross_attention_layouts_and_scale():
     kt, vt = k.transpose(0, 1).contiguous().transpose(0, 1), v.transpose(0, 1).contiguous().transpose(0, 1)
     abi.hsa_cross_attention(ctx, q, st, 320, B, kt, vt, S, o, scale=0.3)
     assert torch.equal(o, want)
+    # equal parts without offsets, for many queries and for few
+    for n in (318, 6):
+        e = torch.tensor([0, n // 3, 2 * n // 3, n], dtype=torch.int32, device="cuda")
+        abi.hsa_cross_attention(ctx, q, e, n, B, k, v, S, want)
+        abi.hsa_cross_attention(ctx, q, None, n, B, k, v, S, o)
+        assert torch.equal(o[:n], want[:n])
+    _refused(1, abi.hsa_cross_attention, ctx, q, None, 320, B, k, v, S, o)
     k1, v1 = k[:1].expand(B, S, H * d), v[:1].expand(B, S, H * d)
     abi.hsa_cross_attention(ctx, q, st, 320, B, k1, v1, S, o)
     abi.hsa_cross_attention(ctx, q, st, 320, B, k1.contiguous(), v1.contiguous(), S, want)

@@ -24,6 +24,7 @@ SYMBOLS = [
     "hsa_ln_gather_mod", "hsa_out_proj_residual_gated", "hsa_mlp_residual_mod",
     "hsa_layer_forward", "hsa_layer_forward_cond", "hsa_quant_rows", "hsa_linear_quant",
     "hsa_ln_gather_quant", "hsa_rope_table", "hsa_rope", "hsa_qk_norm_rope", "hsa_cross_attention",
+    "hsa_layer_forward_ext", "hsa_step_ext",
     "hsa_embed", "hsa_head", "hsa_euler_step", "hsa_euler_step_score", "hsa_step", "hsa_step_cond",
     "hsa_select_groups_static",
 ]
@@ -80,6 +81,18 @@ class hsa_cross_args(ctypes.Structure):
                 ("bs_v", ctypes.c_int64), ("S", ctypes.c_int), ("kv_heads", ctypes.c_int),
                 ("kv_len", ctypes.c_void_p), ("kv_mask", ctypes.c_void_p),
                 ("scale", ctypes.c_float), ("o", ctypes.c_void_p)]
+
+
+class hsa_layer_weights_quant(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("w_qkv", "w_o", "w_1", "w_2", "s_qkv", "s_o",
+                                               "s_1", "s_2")]
+
+
+class hsa_block_ext(ctypes.Structure):
+    _fields_ = [("mod", ctypes.c_void_p), ("xa", ctypes.POINTER(hsa_cross_attn)),
+                ("txt_len", ctypes.c_void_p), ("txt_mask", ctypes.c_void_p),
+                ("qk", ctypes.POINTER(hsa_qk_rope)),
+                ("wq", ctypes.POINTER(hsa_layer_weights_quant))]
 
 
 ROPE_LAYOUT = {"interleaved": 0, "half": 1}
@@ -162,6 +175,10 @@ def load() -> ctypes.CDLL:
         "hsa_qk_norm_rope": (I, [P, ctypes.POINTER(hsa_qk_rope), P, P, I, P, L, P, P, L, P, P, L,
                                  P]),
         "hsa_cross_attention": (I, [P, ctypes.POINTER(hsa_cross_args)]),
+        "hsa_layer_forward_ext": (I, [P, ctypes.POINTER(hsa_layer_weights),
+                                      ctypes.POINTER(hsa_block_ext), P, P, I, P, P]),
+        "hsa_step_ext": (I, [P, ctypes.POINTER(hsa_model_weights), ctypes.POINTER(hsa_state),
+                             ctypes.POINTER(hsa_block_ext), I, F, F, I]),
         "hsa_embed": (I, [P, P, P, P, I, P]),
         "hsa_head": (I, [P, P, P, P, I, P]),
         "hsa_euler_step": (I, [P, P, P, P, P, P, F, F]),
@@ -567,7 +584,7 @@ def _padded(ctx: Context, t, B: int, S: int, width: int, what: str):
 
 def hsa_cross_attention(ctx: Context, q, q_start, n: int, B: int, k, v, S: int, o, kv_len=None,
                         kv_mask=None, kv_heads: Optional[int] = None, scale: float = 0.0) -> None:
-    """q, o bf16 [n, D]; q_start int32 [B + 1]; k, v bf16 [B, S, kv_heads * D/H] (rows and
+    """q, o bf16 [n, D]; q_start int32 [B + 1] or None (n / B rows each); k, v bf16 [B, S, kv_heads * D/H] (rows and
     sequences may be strided, a sequence distance of 0 shares one); kv_len int32 [B];
     kv_mask uint8 or bool [B, S], non-zero = seen (include/hsa.h)."""
     D, H = ctx.cfg.D, ctx.cfg.H
@@ -584,6 +601,51 @@ def hsa_cross_attention(ctx: Context, q, q_start, n: int, B: int, k, v, S: int, 
                           _typed(ctx, kv_mask, B * S, "uint8", "kv_mask"), scale,
                           _typed(ctx, o, n * D, "bfloat16", "o"))
     _check(ctx.ptr, load().hsa_cross_attention(ctx.ptr, ctypes.byref(args)))
+
+
+def quantize_weight(ctx: Context, w):
+    """(int8, scale) of a weight [out, in] (bf16 or fp32), one scale per output channel, rows
+    padded to a multiple of 16 bytes (hsa_quant_rows)."""
+    import torch
+    n, K = w.shape
+    q = torch.zeros((n, (K + 15) // 16 * 16), dtype=torch.int8, device=w.device)
+    scale = torch.empty((n,), dtype=torch.float32, device=w.device)
+    hsa_quant_rows(ctx, w, n, K, q, scale)
+    return q, scale
+
+
+def layer_weights_quant(ctx: Context, w_qkv, w_o, w_1, w_2) -> hsa_layer_weights_quant:
+    """A block's bf16 weights quantised to 8 bits; the struct keeps its tensors alive."""
+    pairs = [quantize_weight(ctx, w) for w in (w_qkv, w_o, w_1, w_2)]
+    s = hsa_layer_weights_quant(*[q.data_ptr() for q, _ in pairs],
+                                *[t.data_ptr() for _, t in pairs])
+    s._keep = pairs
+    return s
+
+
+def block_ext(mod=None, xa: Optional[hsa_cross_attn] = None, txt_len=None, txt_mask=None,
+              qk: Optional[hsa_qk_rope] = None,
+              wq: Optional[hsa_layer_weights_quant] = None) -> hsa_block_ext:
+    """What a block has beyond hsa_layer_forward (include/hsa.h); keeps its parts alive.
+
+    mod: device fp32 [6, D]; txt_len: device int32 [1]; txt_mask: device uint8 [n_txt]."""
+    n_txt = 0 if xa is None else xa.n_txt
+    s = hsa_block_ext(_typed(None, mod, 1, "float32", "mod"),
+                      ctypes.pointer(xa) if xa is not None else None,
+                      _typed(None, txt_len, 1, "int32", "txt_len"),
+                      _typed(None, txt_mask, n_txt, "uint8", "txt_mask"),
+                      ctypes.pointer(qk) if qk is not None else None,
+                      ctypes.pointer(wq) if wq is not None else None)
+    s._keep = (mod, xa, txt_len, txt_mask, qk, wq)
+    return s
+
+
+def hsa_layer_forward_ext(ctx: Context, w: Optional[hsa_layer_weights],
+                          ext: Optional[hsa_block_ext], x, idx, n: int, k_cache, v_cache) -> None:
+    _check(ctx.ptr, load().hsa_layer_forward_ext(
+        ctx.ptr, ctypes.byref(w) if w is not None else None,
+        ctypes.byref(ext) if ext is not None else None, _p(x), _p(idx), n, _p(k_cache),
+        _p(v_cache)))
 
 
 def hsa_embed(ctx: Context, w_in, x_lat, idx, n: int, h) -> None:
@@ -651,6 +713,24 @@ def hsa_step_cond(ctx: Context, model: ModelBinding, cond: Optional[StepCond], i
         ctx.ptr, ctypes.byref(model.weights), ctypes.byref(model.state),
         ctypes.byref(cond.struct) if cond is not None else None, i, float(sigma_i),
         float(sigma_next), 1 if regroup else 0))
+
+
+class StepExt:
+    """The L block extensions of one iteration (keeps them alive)."""
+
+    def __init__(self, exts: Sequence[hsa_block_ext]):
+        self.array = (hsa_block_ext * max(len(exts), 1))(*exts)
+        self._keep = list(exts)
+
+
+def hsa_step_ext(ctx: Context, model: ModelBinding, ext: Optional[StepExt], i: int,
+                 sigma_i: float, sigma_next: float, regroup: bool = True) -> None:
+    if ext is not None and len(ext._keep) != ctx.cfg.L:
+        raise ValueError(f"{len(ext._keep)} block extensions for {ctx.cfg.L} layers")
+    _check(ctx.ptr, load().hsa_step_ext(
+        ctx.ptr, ctypes.byref(model.weights), ctypes.byref(model.state),
+        ext.array if ext is not None else None, i, float(sigma_i), float(sigma_next),
+        1 if regroup else 0))
 
 
 def hsa_select_groups_static(v_prev, v_cur, N: int, counts: Sequence[int], g, stream=None) -> None:

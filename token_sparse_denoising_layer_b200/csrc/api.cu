@@ -152,6 +152,33 @@ bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t depth, uint6
 
 }  // namespace hsa
 
+namespace {
+
+// One iteration; `layer(l, n)` runs block l on the n active rows.
+template <typename Layer>
+hsa_status step(hsa_ctx* ctx, const hsa_model_weights* w, const hsa_state* s, int i, float sigma_i,
+                float sigma_next, int regroup, Layer layer) {
+  int n = 0;
+  hsa_status st = hsa_schedule(ctx, i, s->g, s->mask, s->active_idx, nullptr, &n);
+  if (st == HSA_OK) st = hsa_embed(ctx, w->w_in, s->x, s->active_idx, n, s->h);
+  for (int l = 0; st == HSA_OK && l < ctx->c.cfg.L; ++l) st = layer(l, n);
+  if (st == HSA_OK) st = hsa_head(ctx, w->w_head, s->h, s->active_idx, n, s->v_fresh);
+  // re-grouping from iteration T / s_K on (every token then has two cached
+  // velocities), not after the last; its score is written by the Euler pass
+  const int from = ctx->c.T / ctx->c.budgets[ctx->c.K - 1];
+  const bool regroup_now = regroup && i >= from && i < ctx->c.T - 1;
+  if (st == HSA_OK && !regroup_now)
+    st = hsa_euler_step(ctx, s->x, s->v_hat, s->v_hat_prev, s->v_fresh, s->mask, sigma_i,
+                        sigma_next);
+  if (st == HSA_OK && regroup_now)
+    st = hsa_euler_step_score(ctx, s->x, s->v_hat, s->v_hat_prev, s->v_fresh, s->mask, sigma_i,
+                              sigma_next, s->score);
+  if (st == HSA_OK && regroup_now) st = hsa_select_from_score(ctx, s->score, s->g);
+  return st;
+}
+
+}  // namespace
+
 extern "C" {
 
 const char* hsa_last_error(const hsa_ctx* ctx) {
@@ -209,6 +236,8 @@ hsa_status hsa_create(const hsa_model_cfg* cfg, int T, const int* budgets, const
   if (e == cudaSuccess) e = cudaMalloc(&x.o, nd);
   if (e == cudaSuccess) e = cudaMalloc(&x.hmid, nf);
   if (e == cudaSuccess)
+    e = cudaMalloc(reinterpret_cast<void**>(&x.row_scale), static_cast<size_t>(c.N) * sizeof(float));
+  if (e == cudaSuccess)
     e = cudaMalloc(reinterpret_cast<void**>(&x.attn_part_o),
                    static_cast<size_t>(hsa::kMaxAttnParts) * 256 * 128 * sizeof(float));
   if (e == cudaSuccess)
@@ -239,6 +268,7 @@ void hsa_destroy(hsa_ctx* ctx) {
   cudaFree(x.q);
   cudaFree(x.o);
   cudaFree(x.hmid);
+  cudaFree(x.row_scale);
   cudaFree(x.attn_part_o);
   cudaFree(x.attn_part_ml);
   cudaFree(x.cuts);
@@ -653,56 +683,6 @@ hsa_status hsa_mlp_residual(hsa_ctx* ctx, const void* w_1, const void* w_2, floa
   return mlp_residual(ctx, w_1, w_2, x, idx, n, nullptr, nullptr, nullptr);
 }
 
-hsa_status hsa_layer_forward(hsa_ctx* ctx, const hsa_layer_weights* w, float* x,
-                             const int32_t* idx, int n, void* k_cache, void* v_cache) {
-  return hsa_layer_forward_cond(ctx, w, nullptr, nullptr, x, idx, n, k_cache, v_cache);
-}
-
-hsa_status hsa_layer_forward_cond(hsa_ctx* ctx, const hsa_layer_weights* w, const float* mod,
-                                  const hsa_cross_attn* xa, float* x, const int32_t* idx, int n,
-                                  void* k_cache, void* v_cache) {
-  HSA_CHECK_CTX(ctx);
-  if (w == nullptr) return fail(ctx, HSA_ERR_INVALID_ARG, "w is NULL");
-  if (hsa_status st = check_n(ctx, n)) return st;
-  if (mod != nullptr && (reinterpret_cast<uintptr_t>(mod) & 15) != 0)
-    return fail(ctx, HSA_ERR_INVALID_ARG, "mod must be 16-byte aligned");
-  if (xa != nullptr) {
-    if (xa->n_txt <= 0) return fail(ctx, HSA_ERR_SHAPE, "cross-attention needs n_txt >= 1");
-    HSA_CHECK_PTR(ctx, xa->w_q);
-    HSA_CHECK_PTR(ctx, xa->w_o);
-    HSA_CHECK_PTR(ctx, xa->k_txt);
-    HSA_CHECK_PTR(ctx, xa->v_txt);
-  }
-  if (n == 0) return HSA_OK;
-  Ctx& c = ctx->c;
-  const int D = c.cfg.D;
-  // mod rows: shift_a, scale_a, gate_a, shift_m, scale_m, gate_m.
-  const float* m = mod;
-  auto row = [&](int r) { return m == nullptr ? nullptr : m + static_cast<size_t>(r) * D; };
-  HSA_CHECK_PTR(ctx, x);
-  HSA_CHECK_PTR(ctx, idx);
-  cudaError_t e = hsa::launch_ln_gather(c, x, idx, n, c.u, row(0), row(1));
-  if (e != cudaSuccess) return cuda_fail(ctx, e, "ln_gather");
-  hsa_status st = hsa_qkv_project(ctx, w->w_qkv, c.u, idx, n, c.q, k_cache, v_cache);
-  if (st == HSA_OK) st = hsa_attention(ctx, c.q, n, k_cache, v_cache, c.o);
-  if (st == HSA_OK) {
-    HSA_CHECK_PTR(ctx, w->w_o);
-    st = proj_residual(ctx, w->w_o, c.o, idx, n, x, row(2), "out_proj");
-  }
-  if (st == HSA_OK && xa != nullptr) {
-    e = hsa::launch_ln_gather(c, x, idx, n, c.u);
-    if (e != cudaSuccess) return cuda_fail(ctx, e, "ln_gather");
-    st = hsa_linear(ctx, c.u, n, D, xa->w_q, D, c.q);
-    if (st == HSA_OK) st = hsa_attention_kv(ctx, c.q, n, xa->k_txt, xa->v_txt, xa->n_txt, c.o);
-    if (st == HSA_OK) st = proj_residual(ctx, xa->w_o, c.o, idx, n, x, nullptr, "cross_out_proj");
-  }
-  if (st == HSA_OK) {
-    HSA_CHECK_PTR(ctx, w->w_1);
-    HSA_CHECK_PTR(ctx, w->w_2);
-    st = mlp_residual(ctx, w->w_1, w->w_2, x, idx, n, row(3), row(4), row(5));
-  }
-  return st;
-}
 
 namespace {
 
@@ -925,7 +905,8 @@ hsa_status hsa_cross_attention(hsa_ctx* ctx, const hsa_cross_args* a) {
     return fail(ctx, HSA_ERR_INVALID_ARG, "scale must be finite and >= 0");
   if (a->n == 0) return HSA_OK;
   HSA_CHECK_PTR(ctx, a->q);
-  HSA_CHECK_PTR(ctx, a->q_start);
+  if (a->q_start == nullptr ? a->n % a->B != 0 : !aligned16(a->q_start))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "q_start is not 16-byte aligned, or n is not a multiple of B without it");
   HSA_CHECK_PTR(ctx, a->k);
   HSA_CHECK_PTR(ctx, a->v);
   HSA_CHECK_PTR(ctx, a->o);
@@ -934,6 +915,195 @@ hsa_status hsa_cross_attention(hsa_ctx* ctx, const hsa_cross_args* a) {
   hsa::DeviceScope dev(ctx->c.device);
   std::string why;
   return launched(ctx, hsa::launch_cross_attention(ctx->c, *a, &why), "cross_attention", why);
+}
+
+hsa_status hsa_layer_forward(hsa_ctx* ctx, const hsa_layer_weights* w, float* x,
+                             const int32_t* idx, int n, void* k_cache, void* v_cache) {
+  return hsa_layer_forward_ext(ctx, w, nullptr, x, idx, n, k_cache, v_cache);
+}
+
+hsa_status hsa_layer_forward_cond(hsa_ctx* ctx, const hsa_layer_weights* w, const float* mod,
+                                  const hsa_cross_attn* xa, float* x, const int32_t* idx, int n,
+                                  void* k_cache, void* v_cache) {
+  hsa_block_ext ext{};
+  ext.mod = mod;
+  ext.xa = xa;
+  return hsa_layer_forward_ext(ctx, w, &ext, x, idx, n, k_cache, v_cache);
+}
+
+namespace {
+
+// A product of the context's 8-bit rows in c.u (or `a`), M x Kd, with w.
+hsa::GemmArgs quant_product(const Ctx& c, const void* a, int64_t ld_a, int M, int Kd,
+                            const int8_t* w, const float* w_scale, int Ncols, int epi) {
+  hsa::GemmArgs g{};
+  g.A = a;
+  g.B = w;
+  g.M = M;
+  g.Ncols = Ncols;
+  g.Kd = Kd;
+  g.epi = epi;
+  g.N = c.cfg.N;
+  g.a_scale = c.row_scale;
+  g.b_scale = w_scale;
+  g.ld_a = ld_a;
+  g.ld_b = Kd;
+  return g;
+}
+
+// The block's four products in 8 bits.
+hsa_status quant_qkv(hsa_ctx* ctx, const hsa_layer_weights_quant& w, const float* x,
+                     const int32_t* idx, int n, const float* shift, const float* mscale,
+                     void* k_cache, void* v_cache) {
+  Ctx& c = ctx->c;
+  const int D = c.cfg.D;
+  auto* u = static_cast<int8_t*>(c.u);
+  cudaError_t e = hsa::launch_ln_gather_quant(c, x, idx, n, u, c.row_scale, shift, mscale);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "ln_gather_quant");
+  hsa::GemmArgs g = quant_product(c, u, D, n, D, w.w_qkv, w.s_qkv, 3 * D, hsa::EPI_QKV);
+  g.out = c.q;
+  g.ld_out = D;
+  g.k_cache = k_cache;
+  g.v_cache = v_cache;
+  g.idx = idx;
+  std::string why;
+  return launched(ctx, hsa::launch_gemm_s8(c, g, &why), "qkv_project", why);
+}
+
+hsa_status quant_residual(hsa_ctx* ctx, const void* a, int64_t ld_a, int n, int Kd, const int8_t* w,
+                          const float* s, float* x, const int32_t* idx, const float* gate,
+                          const char* what) {
+  Ctx& c = ctx->c;
+  hsa::GemmArgs g = quant_product(c, a, ld_a, n, Kd, w, s, c.cfg.D, hsa::EPI_RESID);
+  g.x = x;
+  g.ld_x = c.cfg.D;
+  g.gate = gate;
+  g.idx = idx;
+  std::string why;
+  return launched(ctx, hsa::launch_gemm_s8(c, g, &why), what, why);
+}
+
+hsa_status quant_out_proj(hsa_ctx* ctx, const hsa_layer_weights_quant& w, float* x,
+                          const int32_t* idx, int n, const float* gate) {
+  Ctx& c = ctx->c;
+  const int D = c.cfg.D;
+  auto* u = static_cast<int8_t*>(c.u);
+  const cudaError_t e = hsa::launch_quant_rows(c, c.o, false, n, D, D, u, D, c.row_scale);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "quant_rows");
+  return quant_residual(ctx, u, D, n, D, w.w_o, w.s_o, x, idx, gate, "out_proj");
+}
+
+hsa_status quant_mlp(hsa_ctx* ctx, const hsa_layer_weights_quant& w, float* x, const int32_t* idx,
+                     int n, const float* shift, const float* mscale, const float* gate) {
+  Ctx& c = ctx->c;
+  const int D = c.cfg.D, F = c.cfg.F;
+  auto* u = static_cast<int8_t*>(c.u);
+  cudaError_t e = hsa::launch_ln_gather_quant(c, x, idx, n, u, c.row_scale, shift, mscale);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "ln_gather_quant");
+  hsa::GemmArgs up = quant_product(c, u, D, n, D, w.w_1, w.s_1, F, hsa::EPI_GELU);
+  up.out = c.hmid;
+  up.ld_out = F;
+  std::string why;
+  e = hsa::launch_gemm_s8(c, up, &why);
+  if (e != cudaSuccess) return launched(ctx, e, "mlp_up", why);
+  // the hidden rows are quantised over themselves: row m's bytes lie in its own first half
+  auto* h = static_cast<int8_t*>(c.hmid);
+  e = hsa::launch_quant_rows(c, c.hmid, false, n, F, F, h, 2 * static_cast<int64_t>(F), c.row_scale);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "quant_rows");
+  return quant_residual(ctx, h, 2 * static_cast<int64_t>(F), n, F, w.w_2, w.s_2, x, idx, gate, "mlp_down");
+}
+
+}  // namespace
+
+hsa_status hsa_layer_forward_ext(hsa_ctx* ctx, const hsa_layer_weights* w, const hsa_block_ext* ext,
+                                 float* x, const int32_t* idx, int n, void* k_cache, void* v_cache) {
+  HSA_CHECK_CTX(ctx);
+  const hsa_block_ext b = ext != nullptr ? *ext : hsa_block_ext{};
+  const float* mod = b.mod;
+  const hsa_cross_attn* xa = b.xa;
+  if (w == nullptr && b.wq == nullptr) return fail(ctx, HSA_ERR_INVALID_ARG, "w is NULL");
+  if (hsa_status st = check_n(ctx, n)) return st;
+  if (mod != nullptr && (reinterpret_cast<uintptr_t>(mod) & 15) != 0)
+    return fail(ctx, HSA_ERR_INVALID_ARG, "mod must be 16-byte aligned");
+  if (xa != nullptr) {
+    if (xa->n_txt <= 0) return fail(ctx, HSA_ERR_SHAPE, "cross-attention needs n_txt >= 1");
+    HSA_CHECK_PTR(ctx, xa->w_q);
+    HSA_CHECK_PTR(ctx, xa->w_o);
+    HSA_CHECK_PTR(ctx, xa->k_txt);
+    HSA_CHECK_PTR(ctx, xa->v_txt);
+  } else if (b.txt_len != nullptr || b.txt_mask != nullptr) {
+    return fail(ctx, HSA_ERR_INVALID_ARG, "txt_len and txt_mask need xa");
+  }
+  Ctx& c = ctx->c;
+  const int D = c.cfg.D;
+  if (b.wq != nullptr) {
+    if (D > hsa::kMaxLnQuantD || c.cfg.F > hsa::kMaxInPlaceK)
+      return fail(ctx, HSA_ERR_SHAPE, "8-bit block weights need D <= 5120 and F <= 36864");
+    const void* need[8] = {b.wq->w_qkv, b.wq->w_o, b.wq->w_1, b.wq->w_2,
+                           b.wq->s_qkv, b.wq->s_o, b.wq->s_1, b.wq->s_2};
+    for (const void* p : need)
+      if (!aligned16(p))
+        return fail(ctx, HSA_ERR_INVALID_ARG, "an 8-bit weight or scale is NULL or not 16-byte aligned");
+  }
+  if (n == 0) return HSA_OK;
+  // mod rows: shift_a, scale_a, gate_a, shift_m, scale_m, gate_m.
+  const float* m = mod;
+  auto row = [&](int r) { return m == nullptr ? nullptr : m + static_cast<size_t>(r) * D; };
+  HSA_CHECK_PTR(ctx, x);
+  HSA_CHECK_PTR(ctx, idx);
+  hsa_status st = HSA_OK;
+  cudaError_t e = cudaSuccess;
+  if (b.wq != nullptr) {
+    HSA_CHECK_PTR(ctx, k_cache);
+    HSA_CHECK_PTR(ctx, v_cache);
+    st = quant_qkv(ctx, *b.wq, x, idx, n, row(0), row(1), k_cache, v_cache);
+  } else {
+    e = hsa::launch_ln_gather(c, x, idx, n, c.u, row(0), row(1));
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "ln_gather");
+    st = hsa_qkv_project(ctx, w->w_qkv, c.u, idx, n, c.q, k_cache, v_cache);
+  }
+  if (st == HSA_OK && b.qk != nullptr)
+    st = hsa_qk_norm_rope(ctx, b.qk, idx, nullptr, n, nullptr, 0, c.q, nullptr, 0, k_cache, nullptr, 0,
+                          nullptr);
+  if (st == HSA_OK) st = hsa_attention(ctx, c.q, n, k_cache, v_cache, c.o);
+  if (st == HSA_OK && b.wq != nullptr) {
+    st = quant_out_proj(ctx, *b.wq, x, idx, n, row(2));
+  } else if (st == HSA_OK) {
+    HSA_CHECK_PTR(ctx, w->w_o);
+    st = proj_residual(ctx, w->w_o, c.o, idx, n, x, row(2), "out_proj");
+  }
+  if (st == HSA_OK && xa != nullptr) {
+    e = hsa::launch_ln_gather(c, x, idx, n, c.u);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "ln_gather");
+    st = hsa_linear(ctx, c.u, n, D, xa->w_q, D, c.q);
+    if (st == HSA_OK && (b.txt_len != nullptr || b.txt_mask != nullptr)) {
+      hsa_cross_args a{};
+      a.q = c.q;
+      a.n = n;
+      a.B = 1;
+      a.k = xa->k_txt;
+      a.v = xa->v_txt;
+      a.ld_k = a.ld_v = D;
+      a.bs_k = a.bs_v = 0;
+      a.S = xa->n_txt;
+      a.kv_heads = c.cfg.H;
+      a.kv_len = b.txt_len;
+      a.kv_mask = b.txt_mask;
+      a.o = c.o;
+      st = hsa_cross_attention(ctx, &a);
+    } else if (st == HSA_OK) {
+      st = hsa_attention_kv(ctx, c.q, n, xa->k_txt, xa->v_txt, xa->n_txt, c.o);
+    }
+    if (st == HSA_OK) st = proj_residual(ctx, xa->w_o, c.o, idx, n, x, nullptr, "cross_out_proj");
+  }
+  if (st == HSA_OK && b.wq != nullptr) {
+    st = quant_mlp(ctx, *b.wq, x, idx, n, row(3), row(4), row(5));
+  } else if (st == HSA_OK) {
+    HSA_CHECK_PTR(ctx, w->w_1);
+    HSA_CHECK_PTR(ctx, w->w_2);
+    st = mlp_residual(ctx, w->w_1, w->w_2, x, idx, n, row(3), row(4), row(5));
+  }
+  return st;
 }
 
 hsa_status hsa_embed(hsa_ctx* ctx, const float* w_in, const float* x_lat, const int32_t* idx,
@@ -1002,28 +1172,29 @@ hsa_status hsa_step_cond(hsa_ctx* ctx, const hsa_model_weights* w, const hsa_sta
     return fail(ctx, HSA_ERR_INVALID_ARG, "weights and state must not be NULL");
   if (ctx->c.cfg.L > 0 && (s->k_cache == nullptr || s->v_cache == nullptr))
     return fail(ctx, HSA_ERR_INVALID_ARG, "state needs L cache pointers");
-  int n = 0;
-  hsa_status st = hsa_schedule(ctx, i, s->g, s->mask, s->active_idx, nullptr, &n);
-  if (st == HSA_OK) st = hsa_embed(ctx, w->w_in, s->x, s->active_idx, n, s->h);
-  for (int l = 0; st == HSA_OK && l < ctx->c.cfg.L; ++l) {
+  return step(ctx, w, s, i, sigma_i, sigma_next, regroup, [&](int l, int n) {
     const float* mod = (cond != nullptr && cond->mod != nullptr) ? cond->mod[l] : nullptr;
     const hsa_cross_attn* xa = (cond != nullptr && cond->xa != nullptr) ? &cond->xa[l] : nullptr;
-    st = hsa_layer_forward_cond(ctx, &w->layers[l], mod, xa, s->h, s->active_idx, n,
-                                s->k_cache[l], s->v_cache[l]);
-  }
-  if (st == HSA_OK) st = hsa_head(ctx, w->w_head, s->h, s->active_idx, n, s->v_fresh);
-  // re-grouping from iteration T / s_K on (every token then has two cached
-  // velocities), not after the last; its score is written by the Euler pass
-  const int from = ctx->c.T / ctx->c.budgets[ctx->c.K - 1];
-  const bool regroup_now = regroup && i >= from && i < ctx->c.T - 1;
-  if (st == HSA_OK && !regroup_now)
-    st = hsa_euler_step(ctx, s->x, s->v_hat, s->v_hat_prev, s->v_fresh, s->mask, sigma_i,
-                        sigma_next);
-  if (st == HSA_OK && regroup_now)
-    st = hsa_euler_step_score(ctx, s->x, s->v_hat, s->v_hat_prev, s->v_fresh, s->mask, sigma_i,
-                              sigma_next, s->score);
-  if (st == HSA_OK && regroup_now) st = hsa_select_from_score(ctx, s->score, s->g);
-  return st;
+    return hsa_layer_forward_cond(ctx, &w->layers[l], mod, xa, s->h, s->active_idx, n,
+                                  s->k_cache[l], s->v_cache[l]);
+  });
+}
+
+hsa_status hsa_step_ext(hsa_ctx* ctx, const hsa_model_weights* w, const hsa_state* s,
+                        const hsa_block_ext* ext, int i, float sigma_i, float sigma_next,
+                        int regroup) {
+  HSA_CHECK_CTX(ctx);
+  if (w == nullptr || s == nullptr) return fail(ctx, HSA_ERR_INVALID_ARG, "weights and state must not be NULL");
+  if (ctx->c.cfg.L > 0 && (s->k_cache == nullptr || s->v_cache == nullptr))
+    return fail(ctx, HSA_ERR_INVALID_ARG, "state needs L cache pointers");
+  for (int l = 0; l < ctx->c.cfg.L; ++l)
+    if (w->layers == nullptr && (ext == nullptr || ext[l].wq == nullptr))
+      return fail(ctx, HSA_ERR_INVALID_ARG, "layer " + std::to_string(l) + " has no weights");
+  return step(ctx, w, s, i, sigma_i, sigma_next, regroup, [&](int l, int n) {
+    return hsa_layer_forward_ext(ctx, w->layers != nullptr ? &w->layers[l] : nullptr,
+                                 ext != nullptr ? &ext[l] : nullptr, s->h, s->active_idx, n,
+                                 s->k_cache[l], s->v_cache[l]);
+  });
 }
 
 }  // extern "C"

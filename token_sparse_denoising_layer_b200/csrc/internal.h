@@ -23,6 +23,7 @@ constexpr int kMaxCrossKeys = 1 << 26;
 constexpr int kVecRows = 4;  // rows up to which an 8-bit product streams its weights
 // Longest row of an 8-bit product: 128 * 128 * 131071 still fits 32-bit sums.
 constexpr int kMaxQuantK = 131071;
+constexpr int kMaxInPlaceK = 36864;  // longest bf16 row that is quantised over itself
 constexpr int kMaxLnQuantD = 40 * 128;  // widest row of the LayerNorm that quantises
 
 // Bits a kernel can set in the context's device flag (read by hsa_sync_check).
@@ -60,6 +61,7 @@ struct Ctx {
   void* q = nullptr;      // bf16 [N, D] compact queries
   void* o = nullptr;      // bf16 [N, D] compact attention output
   void* hmid = nullptr;   // bf16 [N, F] compact MLP hidden
+  float* row_scale = nullptr;     // [N] scales of rows quantised to 8 bits
   float* attn_part_o = nullptr;   // [kMaxAttnParts][256][128] attention partial O
   float* attn_part_ml = nullptr;  // [kMaxAttnParts][256][2] partial (max, sum)
   uint32_t* cuts = nullptr;  // selector cut keys, 2 words per cut

@@ -100,6 +100,11 @@ struct CrossParams {
 
 __device__ __forceinline__ int clamped(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
+// First row of sequence b's queries (b = B: one past the last row).
+__device__ __forceinline__ int first_row(const CrossParams& p, int b) {
+  return p.q_start != nullptr ? clamped(__ldg(p.q_start + b), 0, p.n) : b * (p.n / p.B);
+}
+
 // Sequence and rows [q0, q1) of unit u of a head, by a 32-way search over the
 // sequences' first units; q0 >= q1: no rows.  Executed by whole warps.
 __device__ __forceinline__ void unit_rows(const CrossParams& p, int u, int& b, int& q0, int& q1) {
@@ -110,7 +115,7 @@ __device__ __forceinline__ void unit_rows(const CrossParams& p, int u, int& b, i
     const int i = lane * step;
     bool at_or_before = false;
     if (i < len)
-      at_or_before = clamped(__ldg(p.q_start + lo + i), 0, p.n) / kUnitQ + lo + i <= u;
+      at_or_before = first_row(p, lo + i) / kUnitQ + lo + i <= u;
     const int c = __popc(__ballot_sync(0xffffffffu, at_or_before));
     if (c == 0) {  // before the first sequence
       b = 0, q0 = 1, q1 = 0;
@@ -121,8 +126,7 @@ __device__ __forceinline__ void unit_rows(const CrossParams& p, int u, int& b, i
     lo = next;
   } while (len > 1);
   b = lo;
-  const int first = clamped(__ldg(p.q_start + b), 0, p.n);
-  const int last = clamped(__ldg(p.q_start + b + 1), 0, p.n);
+  const int first = first_row(p, b), last = first_row(p, b + 1);
   q0 = first + (u - (first / kUnitQ + b)) * kUnitQ;
   q1 = min(last, q0 + kUnitQ);
 }
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0) {  // one CTA looks the offsets and lengths over
     for (int i = threadIdx.x; i < p.B; i += kThreads) {
-      const int a = p.q_start[i], e = p.q_start[i + 1];
+      const int a = p.q_start != nullptr ? p.q_start[i] : 0, e = p.q_start != nullptr ? p.q_start[i + 1] : 0;
       const int len = p.kv_len != nullptr ? p.kv_len[i] : 0;
       if (a < 0 || e > p.n || a > e || len < 0 || len > p.S) atomicOr(p.flag, DEV_BAD_INDEX);
     }

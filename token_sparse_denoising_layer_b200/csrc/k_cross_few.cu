@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(32 * kWarps, R == 1 ? 3 : R == 2 ? 2 : 1) k_cr
 
   if (blockIdx.x == 0) {  // one CTA looks the offsets and lengths over
     for (int i = threadIdx.x; i < p.B; i += 32 * kWarps) {
-      const int a = p.q_start[i], z = p.q_start[i + 1];
+      const int a = p.q_start != nullptr ? p.q_start[i] : 0, z = p.q_start != nullptr ? p.q_start[i + 1] : 0;
       const int len = p.kv_len != nullptr ? p.kv_len[i] : 0;
       if (a < 0 || z > p.n || a > z || len < 0 || len > p.S) atomicOr(p.flag, DEV_BAD_INDEX);
     }
@@ -86,8 +86,9 @@ __global__ void __launch_bounds__(32 * kWarps, R == 1 ? 3 : R == 2 ? 2 : 1) k_cr
   const int rank = blockIdx.x % p.split;
   const int item = blockIdx.x / p.split;
   const int kvh = item % p.kv_heads, b = item / p.kv_heads;
-  const int q0 = clamped(__ldg(p.q_start + b), 0, p.n);
-  const int q1 = clamped(__ldg(p.q_start + b + 1), 0, p.n);
+  const int each = p.n / p.B;  // rows a sequence where q_start is not given
+  const int q0 = p.q_start != nullptr ? clamped(__ldg(p.q_start + b), 0, p.n) : b * each;
+  const int q1 = p.q_start != nullptr ? clamped(__ldg(p.q_start + b + 1), 0, p.n) : q0 + each;
   if (q0 >= q1) return;  // the same for every CTA of the cluster
   const int len = p.kv_len != nullptr ? clamped(__ldg(p.kv_len + b), 0, p.S) : p.S;
   const int rows = (q1 - q0) * p.group;

@@ -251,6 +251,8 @@ void quant_threads(const Ctx& c, const T* a, int64_t ld_a, int n, int Kd, int8_t
   else k_quant_rows<T, TH, 9><<<grid, threads, 0, c.stream>>>(a, ld_a, n, Kd, q, ld_q, scale);
 }
 
+static_assert(kMaxInPlaceK == 9 * 512 * 8, "rows up to here are in registers before they are written");
+
 template <typename T>
 cudaError_t quant_typed(const Ctx& c, const T* a, int n, int Kd, int64_t ld_a, int8_t* q,
                         int64_t ld_q, float* scale) {

@@ -72,22 +72,31 @@ class HsaLoop:
     def n_active(self, i: int) -> int:
         return abi.hsa_n_active(self.ctx, i)
 
-    def step(self, i: int, regroup: bool = True, cond: "Optional[abi.StepCond]" = None) -> None:
+    def step(self, i: int, regroup: bool = True, cond: "Optional[abi.StepCond]" = None,
+             ext: "Optional[abi.StepExt]" = None) -> None:
         """Iteration i; ``cond`` carries conditioned blocks' modulation and
-        cross-attention for this iteration (abi.StepCond), or None."""
-        if cond is None:
+        cross-attention for this iteration (abi.StepCond), or None.  ``ext``
+        (abi.StepExt, in place of cond) adds rotary positions, query/key norms,
+        masked text and 8-bit weights."""
+        if ext is not None:
+            if cond is not None:
+                raise ValueError("give cond or ext, not both")
+            abi.hsa_step_ext(self.ctx, self.model, ext, i, float(self.sigmas[i]),
+                             float(self.sigmas[i + 1]), regroup)
+        elif cond is None:
             abi.hsa_step(self.ctx, self.model, i, float(self.sigmas[i]),
                          float(self.sigmas[i + 1]), regroup)
         else:
             abi.hsa_step_cond(self.ctx, self.model, cond, i, float(self.sigmas[i]),
                               float(self.sigmas[i + 1]), regroup)
 
-    def run(self, regroup: bool = True, stop: Optional[int] = None):
+    def run(self, regroup: bool = True, stop: Optional[int] = None,
+            ext: "Optional[abi.StepExt]" = None):
         for i in range(self.T if stop is None else stop):
-            self.step(i, regroup)
+            self.step(i, regroup, ext=ext)
         return self.x
 
-    def capture(self, regroup: bool = True) -> None:
+    def capture(self, regroup: bool = True, ext: "Optional[abi.StepExt]" = None) -> None:
         """Record the whole loop, i = 0..T-1, as one CUDA graph.
 
         Every step's launch shape is fixed by the host (|A_i| follows from the
@@ -95,6 +104,7 @@ class HsaLoop:
         writes this loop's buffers in place.  Call after at least one eager
         step (first calls set kernel attributes), and reset() before replay()."""
         t = self.torch
+        self._captured_ext = ext  # the graph holds its addresses
         t.cuda.synchronize()
         side = t.cuda.Stream()
         g = t.cuda.CUDAGraph()
@@ -103,7 +113,7 @@ class HsaLoop:
         try:
             with t.cuda.graph(g, stream=side):
                 for i in range(self.T):
-                    self.step(i, regroup)
+                    self.step(i, regroup, ext=ext)
         finally:
             abi.hsa_set_stream(self.ctx, self._stream)
         self.graph_launches = abi.hsa_kernel_launches(self.ctx) - n0
