@@ -517,6 +517,13 @@ def test_cross_attention_rows_of_no_sequence_are_left():
     ref, mag = _cross64(q, starts, k, v, lens, None, 1, 1, 128, 128 ** -0.5)
     _within(o[300:600], ref[300:600], _cross_tol(ref, mag)[300:600])
     assert bool((o[:300] == 6.0).all()) and bool((o[600:] == 6.0).all())
+    few = torch.full_like(q[:7], 6.0)  # the same with a few queries each
+    st = torch.tensor([2, 3, 5], dtype=torch.int32, device="cuda")
+    abi.hsa_cross_attention(ctx, q, st, 7, 2, k, v, 64, few, kv_len=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    abi.hsa_sync_check(ctx)
+    ref, mag = _cross64(q[:7], [2, 3, 5], k, v, lens, None, 1, 1, 128, 128 ** -0.5)
+    _within(few[2:5], ref[2:5], _cross_tol(ref, mag)[2:5])
+    assert bool((few[:2] == 6.0).all()) and bool((few[5:] == 6.0).all())
 
 
 def test_cross_attention_layouts_and_scale():
@@ -675,6 +682,60 @@ def test_no_rows_launch_nothing():
     abi.hsa_qk_norm_rope(ctx, abi.qk_rope(), i, 0, b, b)
     abi.hsa_cross_attention(ctx, b, i, 0, 1, b[None], b[None], 4, b)
     assert abi.hsa_kernel_launches(ctx) == before
+    abi.hsa_sync_check(ctx)
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: their first and last rows."""
+    need_gpu()
+    g = _gen(6)
+    N, H, d = 420000, 40, 128
+    D = H * d  # N * D = 2.15e9
+    ctx = _ctx(N, D, H)
+    idx = torch.tensor([0, 1, N - 2, N - 1], dtype=torch.int32, device="cuda")
+    rows = idx.long()
+    big = torch.zeros(N, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(N, D, dtype=torch.bfloat16, device="cuda")
+    few = _randn(g, 4, D, dtype=torch.bfloat16)
+    table = _table(g, N, 32)
+    # cache rows
+    abi.hsa_qk_norm_rope(ctx, abi.qk_rope(table=table, P=N, rot=32), idx, 4, None, big, k_in=few)
+    ref, tol = _qk_ref(few, None, "head", 1e-6, H, d, table[rows], "half")
+    _within(big[rows], ref, tol)
+    # rotated rows
+    abi.hsa_rope(ctx, big, N, H, table, N, 32, out)
+    ref, mag = _turned(big[rows].double().view(4, H, d), table[rows].double(), "half")
+    _within(out[rows].view(4, H, d), ref, BF * ref.abs() + 4 * F32 * mag)
+    # queries and outputs
+    big[rows] = few
+    k, v = _randn(g, 1, 5, D, dtype=torch.bfloat16), _randn(g, 1, 5, D, dtype=torch.bfloat16)
+    abi.hsa_cross_attention(ctx, big, None, N, 1, k, v, 5, out)
+    ref, mag = _cross64(few, [0, 4], k, v, [5], None, H, H, d, d ** -0.5)
+    _within(out[rows], ref, _cross_tol(ref, mag))
+    # keys far down a cache that all sequences share
+    kv = big.view(1, N, D)
+    st, ln = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([N], dtype=torch.int32, device="cuda")
+    mask = torch.zeros(1, N, dtype=torch.uint8, device="cuda")
+    mask[0, rows] = 1
+    for n, start in ((1, st), (300, None)):
+        q = _randn(g, n, D, dtype=torch.bfloat16)
+        o = torch.empty_like(q)
+        abi.hsa_cross_attention(ctx, q, start, n, 1, kv, kv, N, o, kv_len=ln, kv_mask=mask)
+        ref, mag = _cross64(q, [0, n], few[None], few[None], [4], None, H, H, d, d ** -0.5)
+        _within(o, ref, _cross_tol(ref, mag))
+    # quantised rows, and a product with more than 2^31 outputs
+    q8 = out.view(torch.int8).view(-1)[:N * D].view(N, D)
+    s = torch.empty(N, device="cuda")
+    abi.hsa_quant_rows(ctx, big, N, D, q8, s)
+    want_q, want_s = _quantised(few)
+    assert (q8[rows].cpu().numpy() == want_q).all() and (s[rows].cpu().numpy() == want_s).all()
+    assert bool((s[2:-2] == 0).all())
+    w, sw = torch.randint(-127, 128, (D, 64), generator=g, device="cuda", dtype=torch.int8), torch.ones(D, device="cuda")
+    a = torch.randint(-127, 128, (N, 64), generator=g, device="cuda", dtype=torch.int8)
+    s.fill_(1.0)
+    abi.hsa_linear_quant(ctx, a, s, N, 64, w, sw, D, out)
+    ref = a[rows].double() @ w.double().t()
+    _within(out[rows], ref, (BF + 4 * F32) * ref.abs())
     abi.hsa_sync_check(ctx)
 
 

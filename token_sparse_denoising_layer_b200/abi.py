@@ -257,8 +257,12 @@ def hsa_create(N: int, D: int, H: int, F: int, L: int, T: int, budgets: Sequence
     out = ctypes.c_void_p()
     st = lib.hsa_create(ctypes.byref(cfg), T, b, c, K, m, _stream_ptr(stream), ctypes.byref(out))
     _check(None, st)
-    import torch
-    return Context(out.value, cfg, torch.cuda.current_device())
+    try:
+        import torch
+        device = torch.cuda.current_device()
+    except ImportError:  # a caller with raw addresses and streams only
+        device = None
+    return Context(out.value, cfg, device)
 
 
 def hsa_destroy(ctx: Context) -> None:
