@@ -281,9 +281,16 @@ def test_refusals():
     refused(3, abi.block_ext(xa=bad))
     wide = abi.hsa_create(N=1, D=5248, H=41, F=64, L=0, T=1, budgets=[1], counts=[1])
     one = torch.zeros(5248, device="cuda")
-    with pytest.raises(abi.HsaError) as e:
-        abi.hsa_layer_forward_ext(wide, None, abi.block_ext(wq=abi.layer_weights_quant(c.ctx, *c.w)), one, c.idx, 1, one, one)
-    assert e.value.status == 3
+    need = abi.block_ext(wq=abi.layer_weights_quant(c.ctx, *c.w))
+    with pytest.raises(ValueError):  # another shape's weights
+        abi.hsa_layer_forward_ext(wide, None, need, one, c.idx, 1, one, one)
+    assert abi.load().hsa_layer_forward_ext(wide.ptr, None, need, one.data_ptr(), c.idx.data_ptr(), 1, one.data_ptr(),
+                                            one.data_ptr()) == 3
+    for ext in (abi.block_ext(mod=c.mod[:5].contiguous()), abi.block_ext(qk=abi.qk_rope(table=c.table, P=c.N - 1, rot=c.rot)),
+                abi.block_ext(qk=abi.qk_rope(norm="row", w_q=c.w_q[:64]))):
+        with pytest.raises(ValueError):
+            x, kc, vc = c.state()
+            abi.hsa_layer_forward_ext(c.ctx, c.lw, ext, x, c.idx, c.a, kc, vc)
     with pytest.raises(ValueError):
         abi.block_ext(xa=c.xa, txt_mask=c.mask[:1])
     loop, ext, _, _, _, _ = _ext_loop(False)

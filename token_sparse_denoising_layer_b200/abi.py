@@ -545,9 +545,24 @@ def qk_rope(norm: str = "head", w_q=None, w_k=None, eps: float = 1e-6, table=Non
     """The struct holds raw device addresses, so it also keeps the tensors alive."""
     s = hsa_qk_rope(_choice(QK_NORM, norm, "norm"), _typed(None, w_q, 1, "float32", "w_q"),
                     _typed(None, w_k, 1, "float32", "w_k"), eps,
-                    _typed(None, table, P * rot, "float32", "table"), P, rot, _choice(ROPE_LAYOUT, layout, "layout"))
-    s._keep = (w_q, w_k, table)
+                    _typed(None, table, P * rot, "float32", "table"), P, rot,
+                    _choice(ROPE_LAYOUT, layout, "layout"))
+    s._keep = [t for t in (w_q, w_k, table) if t is not None]
+    s._widths = [t.numel() for t in (w_q, w_k) if t is not None]
+    s._devices = {t.get_device() for t in s._keep}
     return s
+
+
+def _check_qk(ctx: Context, a: hsa_qk_rope) -> None:
+    """The struct's tensors against the context that is to use them."""
+    if a.norm:
+        width = ctx.cfg.D if a.norm == 2 else ctx.cfg.D // ctx.cfg.H
+        for have in getattr(a, "_widths", ()):
+            if have < width:
+                raise ValueError(f"norm weights need {width} elements, have {have}")
+    for where in getattr(a, "_devices", ()):
+        if ctx.device is not None and where != ctx.device:
+            raise ValueError(f"norm weights or table on cuda:{where}, the context on cuda:{ctx.device}")
 
 
 def hsa_qk_norm_rope(ctx: Context, a: hsa_qk_rope, idx, n: int, q, k_cache=None, v_cache=None,
@@ -557,11 +572,7 @@ def hsa_qk_norm_rope(ctx: Context, a: hsa_qk_rope, idx, n: int, q, k_cache=None,
     blocks of a packed [n, 3 D] product; without q_in (k_in) the queries (the
     cache rows idx) change in place."""
     D, N = ctx.cfg.D, ctx.cfg.N
-    w_q, w_k, table = getattr(a, "_keep", (None, None, None))
-    width = 0 if a.norm == 0 else D if a.norm == 2 else D // ctx.cfg.H
-    _typed(ctx, w_q, width, "float32", "w_q")
-    _typed(ctx, w_k, width, "float32", "w_k")
-    _typed(ctx, table, 0, "float32", "table")
+    _check_qk(ctx, a)
     pq, ldq = _rows(ctx, q_in, n, D, ("bfloat16",), "q_in")
     pk, ldk = _rows(ctx, k_in, n, D, ("bfloat16",), "k_in")
     pv, ldv = _rows(ctx, v_in, n, D, ("bfloat16",), "v_in")
@@ -644,8 +655,25 @@ def block_ext(mod=None, xa: Optional[hsa_cross_attn] = None, txt_len=None, txt_m
     return s
 
 
+def _check_ext(ctx: Context, ext: hsa_block_ext) -> None:
+    mod, xa, _, _, qk, wq = ext._keep
+    D, F = ctx.cfg.D, ctx.cfg.F
+    if mod is not None and mod.numel() < 6 * D:
+        raise ValueError(f"mod needs [6, {D}] elements, has {mod.numel()}")
+    if qk is not None:
+        _check_qk(ctx, qk)
+        if qk.table is not None and qk.P < ctx.cfg.N:
+            raise ValueError(f"a block's rotary table needs a row per token: {ctx.cfg.N}, has {qk.P}")
+    if wq is not None:
+        for (q, _), shape in zip(wq._keep, ((3 * D, D), (D, D), (F, D), (D, F))):
+            if tuple(q.shape) != shape:
+                raise ValueError(f"8-bit block weights need shape {shape}, have {tuple(q.shape)}")
+
+
 def hsa_layer_forward_ext(ctx: Context, w: Optional[hsa_layer_weights],
                           ext: Optional[hsa_block_ext], x, idx, n: int, k_cache, v_cache) -> None:
+    if ext is not None:
+        _check_ext(ctx, ext)
     _check(ctx.ptr, load().hsa_layer_forward_ext(
         ctx.ptr, ctypes.byref(w) if w is not None else None,
         ctypes.byref(ext) if ext is not None else None, _p(x), _p(idx), n, _p(k_cache),
@@ -725,12 +753,18 @@ class StepExt:
     def __init__(self, exts: Sequence[hsa_block_ext]):
         self.array = (hsa_block_ext * max(len(exts), 1))(*exts)
         self._keep = list(exts)
+        self._checked_for = None
 
 
 def hsa_step_ext(ctx: Context, model: ModelBinding, ext: Optional[StepExt], i: int,
                  sigma_i: float, sigma_next: float, regroup: bool = True) -> None:
-    if ext is not None and len(ext._keep) != ctx.cfg.L:
-        raise ValueError(f"{len(ext._keep)} block extensions for {ctx.cfg.L} layers")
+    if ext is not None:
+        if len(ext._keep) != ctx.cfg.L:
+            raise ValueError(f"{len(ext._keep)} block extensions for {ctx.cfg.L} layers")
+        if ctx is not ext._checked_for:  # once per context: the structs do not change
+            for e in ext._keep:
+                _check_ext(ctx, e)
+            ext._checked_for = ctx
     _check(ctx.ptr, load().hsa_step_ext(
         ctx.ptr, ctypes.byref(model.weights), ctypes.byref(model.state),
         ext.array if ext is not None else None, i, float(sigma_i), float(sigma_next),

@@ -196,13 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(desc + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0) {  // one CTA looks the offsets and lengths over
-    for (int i = threadIdx.x; i < p.B; i += kThreads) {
-      const int a = p.q_start != nullptr ? p.q_start[i] : 0, e = p.q_start != nullptr ? p.q_start[i + 1] : 0;
-      const int len = p.kv_len != nullptr ? p.kv_len[i] : 0;
-      if (a < 0 || e > p.n || a > e || len < 0 || len > p.S) atomicOr(p.flag, DEV_BAD_INDEX);
-    }
-  }
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -221,19 +214,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_barrier_init();
   }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
-  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // The producer does not wait for the others' start: it set the barriers up
+  // itself and uses no TMEM, so its search and first copies run under the
+  // allocation.
+  uint32_t tmem = 0;
+  if (warp == 0) {
+    __syncwarp();
+    asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+  } else {
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+    tc_fence_after();
+    tmem = *tmem_slot;
+  }
   bool ok = true;
 
   if (warp == 0) {
@@ -414,6 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_base + (t == 0 ? Cfg::kColS0 : Cfg::kColS1);
     const uint32_t tO = tmem + lane_base + (t == 0 ? Cfg::kColO0 : Cfg::kColO1);
     uint8_t* stage = smem + Cfg::kStageAt + (warp - 2) * kStageBytes;
+    if (blockIdx.x == 0) {  // while nothing has arrived yet, one CTA looks the offsets and lengths over
+      for (int i = threadIdx.x - 64; i < p.B; i += 32 * kSoftmaxWarps) {
+        const int a = p.q_start != nullptr ? p.q_start[i] : 0, e = p.q_start != nullptr ? p.q_start[i + 1] : 0;
+        const int len = p.kv_len != nullptr ? p.kv_len[i] : 0;
+        if (a < 0 || e > p.n || a > e || len < 0 || len > p.S) atomicOr(p.flag, DEV_BAD_INDEX);
+      }
+      __syncwarp();
+    }
     int it = 0, ns = 0, no = 0;  // key tiles of the CTA, S tiles and units of this query tile
     for (int nd = 0; ok; ++nd) {
       if (!__all_sync(0xffffffffu, mbar_wait(&d_full[nd & 1], (nd >> 1) & 1))) {

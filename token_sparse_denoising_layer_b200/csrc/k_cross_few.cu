@@ -76,21 +76,18 @@ __global__ void __launch_bounds__(32 * kWarps, R == 1 ? 3 : R == 2 ? 2 : 1) k_cr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane / L, e = 8 * (lane % L);  // key of the warp's step, first place of this lane
 
-  if (blockIdx.x == 0) {  // one CTA looks the offsets and lengths over
-    for (int i = threadIdx.x; i < p.B; i += 32 * kWarps) {
-      const int a = p.q_start != nullptr ? p.q_start[i] : 0, z = p.q_start != nullptr ? p.q_start[i + 1] : 0;
-      const int len = p.kv_len != nullptr ? p.kv_len[i] : 0;
-      if (a < 0 || z > p.n || a > z || len < 0 || len > p.S) atomicOr(p.flag, DEV_BAD_INDEX);
-    }
-  }
   const int rank = blockIdx.x % p.split;
   const int item = blockIdx.x / p.split;
   const int kvh = item % p.kv_heads, b = item / p.kv_heads;
   const int each = p.n / p.B;  // rows a sequence where q_start is not given
-  const int q0 = p.q_start != nullptr ? clamped(__ldg(p.q_start + b), 0, p.n) : b * each;
-  const int q1 = p.q_start != nullptr ? clamped(__ldg(p.q_start + b + 1), 0, p.n) : q0 + each;
+  const int raw0 = p.q_start != nullptr ? __ldg(p.q_start + b) : b * each;
+  const int raw1 = p.q_start != nullptr ? __ldg(p.q_start + b + 1) : raw0 + each;
+  const int raw_len = p.kv_len != nullptr ? __ldg(p.kv_len + b) : p.S;
+  if (threadIdx.x == 0 && (raw0 < 0 || raw1 > p.n || raw0 > raw1 || raw_len < 0 || raw_len > p.S))
+    atomicOr(p.flag, DEV_BAD_INDEX);
+  const int q0 = clamped(raw0, 0, p.n), q1 = clamped(raw1, 0, p.n);
   if (q0 >= q1) return;  // the same for every CTA of the cluster
-  const int len = p.kv_len != nullptr ? clamped(__ldg(p.kv_len + b), 0, p.S) : p.S;
+  const int len = clamped(raw_len, 0, p.S);
   const int rows = (q1 - q0) * p.group;
   const __nv_bfloat16* kb = p.k + b * p.bs_k + kvh * HD + e;
   const __nv_bfloat16* vb = p.v + b * p.bs_v + kvh * HD + e;
