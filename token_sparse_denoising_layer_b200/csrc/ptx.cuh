@@ -511,6 +511,16 @@ __device__ __forceinline__ F2 mul_x2(F2 a, F2 b) {
   return d;
 }
 
+__device__ __forceinline__ F2 add_x2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 __device__ __forceinline__ F2 splat(float v) { return F2{v, v}; }
 
 __device__ __forceinline__ float ex2_approx(float x) {
