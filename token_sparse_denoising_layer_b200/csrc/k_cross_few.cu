@@ -10,7 +10,8 @@
 // sum and output in fp32 (weights are never rounded to 16 bits here), and these are
 // merged over the groups of a warp by shuffles, over the warps of a CTA in shared
 // memory and over the CTAs of a cluster, which split the keys when there are
-// few sequences, through distributed shared memory.
+// few sequences, through distributed shared memory.  16 sequences of one query,
+// 12 heads x 128, up to 512 keys: 12 us (24 in 128-query tiles; the bytes alone take 5.5).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

