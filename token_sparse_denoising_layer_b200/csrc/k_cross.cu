@@ -14,7 +14,7 @@
 //    thirds of its time on its own start and end: the next unit's descriptor, Q
 //    and first keys now arrive while this one's last tile is in softmax, and
 //    its first scores are computed under this one's epilogue.  (26207 queries,
-//    12 heads, 512 and 384 keys: 145 us with a CTA per unit.)
+//    12 heads x 128, 512 and 384 keys: 145 us with a CTA per unit, 91 now.)
 //  - Which rows and keys a unit covers is read on the device.  Units are
 //    numbered per head so that sequence b's first one is
 //    floor(q_start[b] / 256) + b: every sequence has room for its last,
@@ -106,29 +106,42 @@ __device__ __forceinline__ int first_row(const CrossParams& p, int b) {
 }
 
 // Sequence and rows [q0, q1) of unit u of a head, by a 32-way search over the
-// sequences' first units; q0 >= q1: no rows.  Executed by whole warps.
-__device__ __forceinline__ void unit_rows(const CrossParams& p, int u, int& b, int& q0, int& q1) {
+// sequences' first units; q0 >= q1: no rows.  Executed by whole warps.  The last
+// step's lanes hold the rows (and with `len`, the key counts) of all sequences
+// in question, so nothing is loaded again once the sequence is known.
+__device__ __forceinline__ void unit_rows(const CrossParams& p, int u, int& b, int& q0, int& q1,
+                                          int* keys = nullptr) {
   const int lane = threadIdx.x & 31;
   int lo = 0, len = p.B;
-  do {
+  for (;;) {
     const int step = (len + 31) / 32;
     const int i = lane * step;
+    int row = 0, kv = p.S;
     bool at_or_before = false;
-    if (i < len)
-      at_or_before = first_row(p, lo + i) / kUnitQ + lo + i <= u;
+    if (i < len || (step == 1 && i == len)) {  // the one past the last ends it
+      row = first_row(p, lo + i);
+      at_or_before = i < len && row / kUnitQ + lo + i <= u;
+    }
+    if (keys != nullptr && p.kv_len != nullptr && step == 1 && i < len)
+      kv = clamped(__ldg(p.kv_len + lo + i), 0, p.S);
     const int c = __popc(__ballot_sync(0xffffffffu, at_or_before));
     if (c == 0) {  // before the first sequence
       b = 0, q0 = 1, q1 = 0;
       return;
     }
+    if (step == 1) {
+      b = lo + c - 1;
+      const int first = __shfl_sync(0xffffffffu, row, c - 1);
+      const int last = c < 32 ? __shfl_sync(0xffffffffu, row, c & 31) : first_row(p, b + 1);
+      if (keys != nullptr) *keys = __shfl_sync(0xffffffffu, kv, c - 1);
+      q0 = first + (u - (first / kUnitQ + b)) * kUnitQ;
+      q1 = min(last, q0 + kUnitQ);
+      return;
+    }
     const int next = lo + (c - 1) * step;
     len = min(step, lo + len - next);
     lo = next;
-  } while (len > 1);
-  b = lo;
-  const int first = first_row(p, b), last = first_row(p, b + 1);
-  q0 = first + (u - (first / kUnitQ + b)) * kUnitQ;
-  q1 = min(last, q0 + kUnitQ);
+  }
 }
 
 // Bits of the first `left` of a tile's keys.
@@ -196,22 +209,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(desc + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
-    }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);  // one arrival per softmax warp
-      mbar_init(&o_done[t], 1);
-      mbar_init(&d_full[t], 1);
-      mbar_init(&d_empty[t], 1 + kSoftmaxWarps);
-    }
+  // a barrier per lane: q_full .. v_empty, s_full, p_full, o_done, d_full, d_empty
+  constexpr int kP = 4 * kStages + 4, kD = kP + 6;  // first of p_full and of d_empty
+  if (warp == 0 && lane < kD + 2) {
+    mbar_init(bars + lane, lane >= kD ? 1 + kSoftmaxWarps : lane >= kP && lane < kP + 2 ? 4 : 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -248,12 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (item < total) {
         const int unit = item / p.split, piece = item - unit * p.split;
         d.h = unit / p.units_per_head;
-        unit_rows(p, unit - d.h * p.units_per_head, d.b, d.q0, d.q1);
+        int keys = 0;
+        unit_rows(p, unit - d.h * p.units_per_head, d.b, d.q0, d.q1, &keys);
         rows = d.q0 < d.q1;
         if (rows) {
           if (d.b != seen_b) {
             seen_b = d.b;
-            seen_len = p.kv_len != nullptr ? clamped(__ldg(p.kv_len + d.b), 0, p.S) : p.S;
+            seen_len = keys;
             seen_tiles(p, d.b, seen_len, lo_tile, hi_tile);
           }
           d.len = seen_len;
@@ -460,6 +462,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
+      // Zeroes the unseen rows of this tile's V (whatever they hold must not meet a
+      // weight of 0), while the scores are computed.
+      auto clear_unseen = [&](const uint32_t (&see)[4]) {
+        if (t != 0 || (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu) return true;
+        if (!__all_sync(0xffffffffu, mbar_wait(&v_full[it % kStages], (it / kStages) & 1))) return false;
+        const uint32_t mine4 = qd == 0 ? see[0] : qd == 1 ? see[1] : qd == 2 ? see[2] : see[3];
+        if (!((mine4 >> lane) & 1u)) {
+          // eight lanes in a row start from bank groups of their own
+          const int at = (it % kStages) * Cfg::kTileBytes + row * 128 + 16 * (lane & 7);
+#pragma unroll
+          for (int r = 0; r < Cfg::kRegions; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(sV + ((at + r * Cfg::kRegionBytes) ^ (16 * i))) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        return true;
+      };
       load_bytes(d.j0);
       float m_run = -FLT_MAX, l_run = 0.f;
       for (int j = 0; j < d.nkv; ++j, ++it, ++ns) {
@@ -472,23 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           first_bits(d.len - (d.j0 + j) * kKV, see);
         }
         const bool whole = (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu;  // same for all rows
-        if (!whole && t == 0) {
-          // unseen rows of V: whatever they hold must not meet a weight of 0
-          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[it % kStages], (it / kStages) & 1))) {
-            ok = false;
-            break;
-          }
-          const uint32_t mine4 = qd == 0 ? see[0] : qd == 1 ? see[1] : qd == 2 ? see[2] : see[3];
-          if (!((mine4 >> lane) & 1u)) {
-            uint8_t* vrow = sV + (it % kStages) * Cfg::kTileBytes + row * 128;
-#pragma unroll
-            for (int r = 0; r < Cfg::kRegions; ++r)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(vrow + r * Cfg::kRegionBytes + 16 * i) =
-                    make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
+        if (!clear_unseen(see)) {
+          ok = false;
+          break;
         }
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], ns & 1))) {
           ok = false;
