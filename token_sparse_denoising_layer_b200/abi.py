@@ -430,14 +430,15 @@ def _choice(table: dict, name: str, what: str) -> int:
     return table[name]
 
 
-_dtype_names: dict = {}
+_dtype_names: dict = {}  # tensor types by name, and names by type, filled as types are met
 
 
 def _dtype(t) -> str:
-    """Name of a tensor's type ("bfloat16"), looked up once per type."""
+    """Name of a tensor's type ("bfloat16")."""
     name = _dtype_names.get(t.dtype)
     if name is None:
         name = _dtype_names[t.dtype] = str(t.dtype)[len("torch."):]
+        _dtype_names[name] = t.dtype
     return name
 
 
@@ -453,6 +454,9 @@ def _typed(ctx: Optional[Context], t, n: int, dtype: str, what: str) -> Optional
     """Device address of a contiguous tensor of at least n elements of a type."""
     if t is None:
         return None
+    if (ctx is not None and t.dtype is _dtype_names.get(dtype) and t.get_device() == ctx.device
+            and t.numel() >= n and t.is_contiguous()):
+        return t.data_ptr()  # (most calls: a call's checks are a good part of its host time)
     if _dtype(t) != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
     if t.numel() < n:
@@ -467,15 +471,18 @@ def _rows(ctx: Context, t, n: int, width: int, dtypes: Sequence[str], what: str)
     """(address, row distance in elements) of a 2-D tensor with dense rows."""
     if t is None:
         return None, 0
+    shape, stride = t.shape, t.stride()
+    if (len(shape) == 2 and shape[0] >= n and shape[1] >= width and stride[1] == 1
+            and t.get_device() == ctx.device and _dtype_names.get(t.dtype) in dtypes):
+        # a single row has no distance to the next: any legal one will do
+        return t.data_ptr(), stride[0] if shape[0] > 1 else (width + 15) // 16 * 16
     if _dtype(t) not in dtypes:
         raise ValueError(f"{what} must be {' or '.join(dtypes)}, got {t.dtype}")
     _on_device(ctx, t, what)
-    shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] < n or shape[1] < width:
         raise ValueError(f"{what} must be [>= {n}, >= {width}], got {tuple(shape)}")
     if stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{what} must have dense rows")
-    # a single row has no distance to the next: any legal one will do
     return t.data_ptr(), stride[0] if shape[0] > 1 else (width + 15) // 16 * 16
 
 
