@@ -220,25 +220,6 @@ __device__ __forceinline__ void dequant_chunk(uint32_t (&r)[32], float sa, const
   }
 }
 
-// Store a chunk of a bf16 output whose rows are not 16-byte aligned: through
-// shared memory, so that one store instruction covers 32 adjacent columns of
-// one row.
-__device__ __forceinline__ void store_ragged(const EpiParams& p, const uint32_t (&r)[32], int m,
-                                             int col, float* stage) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int e = 0; e < 32; ++e) stage[lane * 32 + ((e + lane) & 31)] = __uint_as_float(r[e]);
-  __syncwarp();
-  const int m0 = m - lane;
-  if (col + lane < p.Ncols) {
-    __nv_bfloat16* dst = p.out + static_cast<size_t>(m0) * p.ld_out + col + lane;
-    const int rows = p.M - m0 < 32 ? p.M - m0 : 32;
-    for (int k = 0; k < rows; ++k, dst += p.ld_out)
-      *dst = __float2bfloat16_rn(stage[k * 32 + ((lane + k) & 31)]);
-  }
-  __syncwarp();  // the stage is reused by the next chunk
-}
-
 // 32 fp32 values of this lane's row -> bf16 in the warp's stage, columns 32 half ..
 // of a row of 64.  The 16-byte group g of row r lies at group g ^ (r & 7):
 // free of bank conflicts by rows and by columns.
@@ -286,6 +267,64 @@ __device__ __forceinline__ void store_half(const EpiParams& p, const uint8_t* st
   __syncwarp();  // the stage is reused by the next tile
 }
 
+// Store staged columns col .. end - 1 (up to 64) of a bf16 output whose rows are
+// not 16-byte aligned, in the widest stores that the row length allows: 8 bytes
+// a lane and two rows an instruction, 4 bytes and one row, or 2 bytes and half a
+// row.  Eight instructions' rows are read before the first is stored.  (5000 x 700 x
+// 3000: 21 us, 3004 25, 3002 31, 3001 30; 4-byte stores from an odd row's first
+// even place on took 43.)
+__device__ __forceinline__ void store_ragged(const EpiParams& p, const uint8_t* stage, int m0,
+                                             int col, int end) {
+  const int lane = threadIdx.x & 31;
+  const int rows = p.M - m0 < 32 ? p.M - m0 : 32;
+  const size_t ld = p.ld_out;
+  auto at = [&](int r, int e) { return stage + r * 128 + 16 * ((e >> 3) ^ (r & 7)) + 2 * (e & 7); };
+  __nv_bfloat16* out = p.out + m0 * ld + col;
+  __syncwarp();
+  if ((p.ld_out & 3) == 0) {
+    const int e = 4 * (lane & 15);
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+      uint2 w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = *reinterpret_cast<const uint2*>(at(r0 + 2 * k + (lane >> 4), e));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = r0 + 2 * k + (lane >> 4);
+        if (r < rows && col + e < end) *reinterpret_cast<uint2*>(out + r * ld + e) = w[k];
+      }
+    }
+  } else if ((p.ld_out & 1) == 0) {
+    const int e = 2 * lane;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = *reinterpret_cast<const uint32_t*>(at(r0 + k, e));
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (r0 + k < rows && col + e < end) *reinterpret_cast<uint32_t*>(out + (r0 + k) * ld + e) = w[k];
+    }
+  } else {
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      uint16_t w[8][2];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        w[k][0] = *reinterpret_cast<const uint16_t*>(at(r0 + k, lane));
+        w[k][1] = *reinterpret_cast<const uint16_t*>(at(r0 + k, lane + 32));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint16_t* dst = reinterpret_cast<uint16_t*>(out + (r0 + k) * ld);
+        if (r0 + k < rows && col + lane < end) dst[lane] = w[k][0];
+        if (r0 + k < rows && col + lane + 32 < end) dst[lane + 32] = w[k][1];
+      }
+    }
+  }
+  __syncwarp();  // the stage is reused by the next 64 columns
+}
+
 // Drain one accumulator tile: this warp's 32 rows (TMEM lanes at tbase),
 // output row m (this lane's), columns n0 .. n0 + kCols - 1.  TMEM loads run
 // one 32-column chunk ahead of the chunk being stored.  `sa` is the row's scale
@@ -318,18 +357,21 @@ __device__ __forceinline__ void drain_tile(const EpiParams& p, const CUtensorMap
     if (col >= p.Ncols) continue;  // uniform over the warp
     if (kS8) dequant_chunk(cur, sa, sb);
     if (kS8 && kEpi == EPI_STORE) {
+      uint8_t* bytes = reinterpret_cast<uint8_t*>(stage);
+      const int m0 = m - (threadIdx.x & 31);
+      const bool last = c + 1 == NC || col + 32 >= p.Ncols;
+      if (!(c & 1)) {  // the stage may still be on its way out
+        if ((threadIdx.x & 31) == 0) tma_store_wait_read();
+        __syncwarp();
+      }
+      stage_half(bytes, cur, c & 1);
       if ((p.ld_out & 7) != 0) {
-        store_ragged(p, cur, m, col, stage);
-      } else {
-        uint8_t* bytes = reinterpret_cast<uint8_t*>(stage);
-        if (!(c & 1)) {  // the stage may still be on its way out
-          if ((threadIdx.x & 31) == 0) tma_store_wait_read();
-          __syncwarp();
-        }
-        stage_half(bytes, cur, c & 1);
-        const int m0 = m - (threadIdx.x & 31);
-        if (c & 1) store_staged(tm_out, bytes, m0, col - 32);
-        else if (c + 1 == NC || col + 32 >= p.Ncols) store_half(p, bytes, m0, col);
+        if ((c & 1) || last)
+          store_ragged(p, bytes, m0, col - 32 * (c & 1), min(p.Ncols, col + 32));
+      } else if (c & 1) {
+        store_staged(tm_out, bytes, m0, col - 32);
+      } else if (last) {
+        store_half(p, bytes, m0, col);
       }
     } else if (kEpi == EPI_RESID) {
       resid_chunk(p, cur, dst_row, col, stage);
@@ -829,7 +871,8 @@ cudaError_t launch_gemm_s8(const Ctx& c, const GemmArgs& a, std::string* why) {
   if (a.Ncols >= 256 && a.M >= 256) {
     const long tiles = static_cast<long>((a.M + 255) / 256) * ((a.Ncols + 255) / 256);
     const int pairs = c.num_sms / 2;
-    best = static_cast<double>((tiles + pairs - 1) / pairs) * 256 * kPairCost, bn = -1;
+    // (0.75: 700 x 5000 x 8000 takes 46 us in pairs, 54 in 192-wide tiles)
+    best = static_cast<double>((tiles + pairs - 1) / pairs) * 256 * 0.75, bn = -1;
   }
   if (cost(256, 1.0) < best) best = cost(256, 1.0), bn = 256;
   if (cost(192, 1.03) < best) best = cost(192, 1.03), bn = 192;
