@@ -85,6 +85,7 @@ struct Vec8<__nv_bfloat16> {
       if (i < left) r[i >> 1] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
     w = make_uint4(r[0], r[1], r[2], r[3]);
   }
+  __device__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
   __device__ void get(float (&f)[8]) const {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -107,6 +108,7 @@ struct Vec8<float> {
                     left > 3 ? p[3] : 0.f);
     b = make_float4(left > 4 ? p[4] : 0.f, left > 5 ? p[5] : 0.f, left > 6 ? p[6] : 0.f, 0.f);
   }
+  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ void get(float (&f)[8]) const {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
@@ -150,6 +152,81 @@ __global__ void __launch_bounds__(TH == 32 ? 256 : TH, TH == 32 ? 4 : TH == 128 
     v[c].get(f);
     const uint32_t lo = s.x == 0.f ? 0u : quant4(f[0], f[1], f[2], f[3], s.x);
     const uint32_t hi = s.x == 0.f ? 0u : quant4(f[4], f[5], f[6], f[7], s.x);
+    if (e + 8 <= Kd) {
+      *reinterpret_cast<uint2*>(out + e) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (e + i < Kd) out[e + i] = static_cast<int8_t>((i < 4 ? lo >> (8 * i) : hi >> (8 * (i - 4))) & 0xffu);
+    }
+  }
+}
+
+// Rows that start anywhere (an odd Kd, a column block): W warps a row (8 rows of
+// one warp, or one row, per block), NC vectors a lane.  Loads stay whole by starting from the
+// aligned address `skip` values before the row, inside the row before it; each
+// vector's 8 bytes are then joined with those of the next (the next lane's, or
+// the next step's first lane's) and shifted by `skip`, as q's rows are aligned.
+// A warp's last vector only lends its bytes: segments advance by 32 NC - 1
+// vectors.  20000 x 1001 bf16: 17 us, 38 with 2-byte loads (20000 x 1000: 13).
+template <typename T, int W, int NC>
+__global__ void __launch_bounds__(W == 1 ? 256 : 32 * W)
+    k_quant_rows_shift(const T* a, int64_t ld_a, int n, int Kd, int8_t* q, int64_t ld_q, float* scale) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int m = W == 1 ? blockIdx.x * 8 + warp : blockIdx.x;
+  if (m >= n) return;
+  const T* row = a + m * ld_a;
+  const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const int v0 = W == 1 ? 0 : warp * (32 * NC - 1);
+  Vec8<T> v[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (c > 0 && 8 * (v0 + 32 * c) - skip >= Kd) {  // the row ends before this step
+      v[c].zero();
+      continue;
+    }
+    const int at = 8 * (v0 + lane + 32 * c) - skip;  // place of the vector's first value in the row
+    v[c].load(row + at, Kd - at);
+  }
+  const int before = v0 + lane == 0 ? skip : 0;  // values of the first vector that are not the row's
+  uint32_t top = 0u;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float f[8];
+    v[c].get(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c > 0 || i >= before) top = max(top, abs_bits(f[i]));
+  }
+  const float2 s = row_scales(row_top<32 * W>(top));
+  if (lane == 0 && (W == 1 || warp == 0)) scale[m] = s.y;
+  uint32_t w[NC][2];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    w[c][0] = w[c][1] = 0u;
+    if (c > 0 && 8 * (v0 + 32 * c) - skip >= Kd) continue;
+    float f[8];
+    v[c].get(f);
+    w[c][0] = s.x == 0.f ? 0u : quant4(f[0], f[1], f[2], f[3], s.x);
+    w[c][1] = s.x == 0.f ? 0u : quant4(f[4], f[5], f[6], f[7], s.x);
+  }
+  int8_t* out = q + m * ld_q;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (8 * (v0 + 32 * c) >= Kd) break;
+    uint32_t next = __shfl_down_sync(0xffffffffu, w[c][0], 1);
+    uint32_t next2 = __shfl_down_sync(0xffffffffu, w[c][1], 1);
+    if (c + 1 < NC) {
+      const uint32_t x = __shfl_sync(0xffffffffu, w[c + 1 < NC ? c + 1 : c][0], 0);
+      const uint32_t y = __shfl_sync(0xffffffffu, w[c + 1 < NC ? c + 1 : c][1], 0);
+      if (lane == 31) next = x, next2 = y;
+    } else if (lane == 31) {
+      continue;
+    }
+    const bool far = skip >= 4;
+    const uint32_t x = far ? w[c][1] : w[c][0], y = far ? next : w[c][1], z = far ? next2 : next;
+    const uint32_t lo = __funnelshift_r(x, y, 8 * (skip & 3)), hi = __funnelshift_r(y, z, 8 * (skip & 3));
+    const int e = 8 * (v0 + lane + 32 * c);
     if (e + 8 <= Kd) {
       *reinterpret_cast<uint2*>(out + e) = make_uint2(lo, hi);
     } else {
@@ -260,6 +337,13 @@ void quant_threads(const Ctx& c, const T* a, int64_t ld_a, int n, int Kd, int8_t
   else k_quant_rows<T, TH, 9><<<grid, threads, 0, c.stream>>>(a, ld_a, n, Kd, q, ld_q, scale);
 }
 
+template <typename T, int W, int NC>
+void quant_shift(const Ctx& c, const T* a, int64_t ld_a, int n, int Kd, int8_t* q, int64_t ld_q,
+                 float* scale) {
+  k_quant_rows_shift<T, W, NC><<<W == 1 ? (n + 7) / 8 : n, W == 1 ? 256 : 32 * W, 0, c.stream>>>(
+      a, ld_a, n, Kd, q, ld_q, scale);
+}
+
 static_assert(kMaxInPlaceK == 9 * 512 * 8, "rows up to here are in registers before they are written");
 
 template <typename T>
@@ -270,6 +354,14 @@ cudaError_t quant_typed(const Ctx& c, const T* a, int n, int Kd, int64_t ld_a, i
   if (vec && vecs <= 9 * 32) quant_threads<T, 32>(c, a, ld_a, n, Kd, q, ld_q, scale);
   else if (vec && vecs <= 9 * 128) quant_threads<T, 128>(c, a, ld_a, n, Kd, q, ld_q, scale);
   else if (vec && vecs <= 9 * 512) quant_threads<T, 512>(c, a, ld_a, n, Kd, q, ld_q, scale);
+  else if (vecs <= 32 * 2 - 1) quant_shift<T, 1, 2>(c, a, ld_a, n, Kd, q, ld_q, scale);
+  else if (vecs <= 32 * 4 - 1) quant_shift<T, 1, 4>(c, a, ld_a, n, Kd, q, ld_q, scale);
+  else if (vecs <= 32 * 8 - 1) quant_shift<T, 1, 8>(c, a, ld_a, n, Kd, q, ld_q, scale);
+  else if (vecs <= 4 * (32 * 3 - 1)) quant_shift<T, 4, 3>(c, a, ld_a, n, Kd, q, ld_q, scale);
+  else if (vecs <= 4 * (32 * 5 - 1)) quant_shift<T, 4, 5>(c, a, ld_a, n, Kd, q, ld_q, scale);
+  else if (vecs <= 4 * (32 * 8 - 1)) quant_shift<T, 4, 8>(c, a, ld_a, n, Kd, q, ld_q, scale);
+  else if (vecs <= 8 * (32 * 8 - 1)) quant_shift<T, 8, 8>(c, a, ld_a, n, Kd, q, ld_q, scale);
+  else if (vecs <= 16 * (32 * 8 - 1)) quant_shift<T, 16, 8>(c, a, ld_a, n, Kd, q, ld_q, scale);
   else k_quant_rows_any<T><<<n, 256, 0, c.stream>>>(a, ld_a, n, Kd, q, ld_q, scale);
   c.launches += 1;
   return cudaGetLastError();
