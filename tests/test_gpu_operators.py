@@ -59,7 +59,7 @@ def _quantised(a):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("n,K", [(1, 1), (3, 7), (9, 8), (130, 129), (33, 1536), (5, 2304), (7, 2312), (6, 8960),
                                  (3, 9217), (2, 40008), (1, 131071), (19, 503), (18, 505), (9, 1015), (9, 1017), (9, 2041),
-                                 (5, 3039), (5, 3041), (6, 4063), (6, 4065), (5, 5087), (5, 5089), (5, 8161), (4, 32639), (4, 32641), (40, 3), (20, 62)])
+                                 (5, 3039), (5, 3041), (6, 4063), (6, 4065), (5, 5087), (5, 5089), (5, 8161), (4, 32639), (4, 32641), (40, 3), (20, 62), (9999, 65), (9475, 248), (9473, 249), (9474, 503)])
 def test_quant_rows(n, K, dtype):
     need_gpu()
     ctx = _ctx()
