@@ -134,9 +134,12 @@ uint64_t hsa_kernel_launches(const hsa_ctx* ctx);
  * running step (no counterpart on the pages: instrumentation).  While on, every
  * kernel launch of the context is bracketed by two CUDA events on its stream
  * and its algorithmic work is added up per class:
- *   0 attention   (hsa_attention, hsa_attention_kv; work = 4 n n_kv D FLOP)
- *   1 GEMM        (QKV, out-projection, MLP, linear; work = 2 M Ncols K FLOP)
- *   2 row kernels (LN gather, KV scatter, embed, head; work = bytes moved)
+ *   0 attention   (hsa_attention, hsa_attention_kv, hsa_cross_attention; work = 4 n n_kv D
+ *                  FLOP, n_kv the padded count where lengths are on the device)
+ *   1 GEMM        (QKV, out-projection, MLP, linear, 8-bit products; work = 2 M Ncols K
+ *                  operations)
+ *   2 row kernels (LN gather, KV scatter, embed, head, quantisation, rotary positions;
+ *                  work = bytes moved)
  *   3 per-token   (schedule, score, selection, Euler; work = 0)
  * hsa_kernel_times synchronises the stream, writes the first n_classes
  * classes' totals (launch calls, summed event milliseconds, work) to out, and

@@ -669,6 +669,36 @@ def test_operators_on_another_stream_and_in_a_graph():
     del graph
 
 
+def test_two_contexts_at_once():
+    """Two contexts on two streams have scratch of their own: their calls may overlap."""
+    need_gpu()
+    H, d, S = 2, 128, 3000
+    D = H * d
+    g = _gen(31)
+    q = _randn(g, 300, D, dtype=torch.bfloat16)
+    k, v = _randn(g, 1, S, D, dtype=torch.bfloat16), _randn(g, 1, S, D, dtype=torch.bfloat16)
+    w = torch.randint(-127, 128, (700, D), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.ones(700, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    for s in streams:
+        ctx = _ctx(1, D, H, stream=s)
+        runs.append((ctx, torch.empty_like(q), torch.empty(300, D, dtype=torch.int8, device="cuda"), torch.empty(300, device="cuda"),
+                     torch.empty(300, 700, dtype=torch.bfloat16, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for ctx, o, q8, s8, y in runs:
+            abi.hsa_cross_attention(ctx, q, None, 300, 1, k, v, S, o)  # split over keys: partial results in scratch
+            abi.hsa_quant_rows(ctx, o, 300, D, q8, s8)
+            abi.hsa_linear_quant(ctx, q8, s8, 300, D, w, sw, 700, y)
+    for ctx, *_ in runs:
+        abi.hsa_sync_check(ctx)
+    ref, mag = _cross64(q, [0, 300], k, v, [S], None, H, H, d, d ** -0.5)
+    for ctx, o, q8, s8, y in runs:
+        _within(o, ref, _cross_tol(ref, mag))
+        assert torch.equal(o, runs[0][1]) and torch.equal(y, runs[0][4])
+
+
 def test_no_rows_launch_nothing():
     need_gpu()
     ctx = _ctx(4, 128, 1)

@@ -26,9 +26,15 @@ namespace hsa {
 
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kBatch = 4;    // keys of a lane group loaded together
 constexpr int kFewRows = 4;  // rows of one pass over the keys
+
+// Warps of a CTA: four rows' states fill the registers of half as many threads
+// (16 sequences, 4 rows a key head, 2000 keys: 24 us with eight warps, 17 with four).
+template <int R>
+constexpr int warps_of() {
+  return R == kFewRows ? 4 : 8;
+}
 
 struct FewParams {
   const __nv_bfloat16 *q, *k, *v;
@@ -68,7 +74,9 @@ struct Run {
 };
 
 template <int HD, int R>
-__global__ void __launch_bounds__(32 * kWarps, R == 1 ? 3 : R == 2 ? 2 : 1) k_cross_few(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(32 * warps_of<R>(), R == 1 ? 3 : 2)
+    k_cross_few(const __grid_constant__ FewParams p) {
+  constexpr int kWarps = warps_of<R>();
   constexpr int L = HD / 8, G = 32 / L;  // lanes per key, keys per warp step
   __shared__ float s_ml[kWarps][R][2];
   __shared__ __align__(16) float s_o[kWarps][R][HD];
@@ -263,7 +271,7 @@ template <int HD, int R>
 cudaError_t launch_rows(const Ctx& c, const FewParams& p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.kv_heads * p.split);
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.blockDim = dim3(32 * warps_of<R>());
   cfg.stream = c.stream;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -282,8 +290,8 @@ cudaError_t launch_cross_few(const Ctx& c, const hsa_cross_args& a, bool* taken)
   const int H = c.cfg.H, hd = c.cfg.D / H, group = H / a.kv_heads;
   const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads;
   // One pass over the keys for a sequence of average length.  With more rows a
-  // 128-query tile is faster although most of it is empty (16 sequences, 512 keys: 4 rows
-  // a key head 25 us here and 40 in tiles, 6 rows 55 and 23).
+  // 128-query tile is faster although most of it is empty (16 sequences: 4 rows a key head,
+  // 2000 keys 17 us here and 40 in tiles; 6 rows, 512 keys 55 and 23).
   const int64_t rows = static_cast<int64_t>(a.n) * group;
   *taken = rows <= static_cast<int64_t>(a.B) * kFewRows && items * 8 < 0x7fffffff;
   if (!*taken) return cudaSuccess;
@@ -310,7 +318,7 @@ cudaError_t launch_cross_few(const Ctx& c, const hsa_cross_args& a, bool* taken)
   p.flag = c.flag;
   // Keys over a cluster while there are fewer than two CTAs an SM and each
   // keeps a batch for every warp.
-  const int batch = kWarps * kBatch * (256 / hd);
+  const int batch = 8 * kBatch * (256 / hd);
   p.split = 1;
   while (p.split < 8 && items * p.split < 2 * c.num_sms && a.S >= 2 * p.split * batch) p.split *= 2;
   const int r = rows <= a.B ? 1 : rows <= 2 * static_cast<int64_t>(a.B) ? 2 : kFewRows;
