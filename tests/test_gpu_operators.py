@@ -527,6 +527,41 @@ def test_cross_attention_rows_of_no_sequence_are_left():
     assert bool((few[:2] == 6.0).all()) and bool((few[5:] == 6.0).all())
 
 
+@pytest.mark.parametrize("H,Hk,d,step,B,S,holes", [
+    (24, 12, 64, 7, 40, 300, 0),    # two heads a tile row
+    (12, 1, 128, 13, 20, 130, 0.2),
+    (32, 4, 64, 16, 30, 513, 0),    # sequences that end with a tile
+    (48, 3, 64, 2, 33, 900, 0.5),
+    (32, 1, 64, 9, 32, 77, 0),
+    (64, 1, 64, 40, 8, 1000, 0.9),  # more heads than are packed
+    (32, 2, 128, 2, 8, 4096, 0),    # and key ranges that are merged
+])
+def test_cross_attention_packs_the_heads_of_a_key_head(H, Hk, d, step, B, S, holes):
+    need_gpu()
+    ctx = _ctx(1, H * d, H)
+    starts, lens = [5], []
+    for b in range(B):  # one sequence without rows, some without keys, lengths around `step`
+        starts.append(starts[-1] + (0 if b == 1 else step + (b % 3 - 1) * (step > 2)))
+        lens.append(0 if b % 5 == 3 else S - 11 * b % S)
+    n = starts[-1] + 3
+    q, k, v, mask = _cross_case(H + S, H, Hk, d, starts, S, lens, holes, n=n)
+    seen = torch.arange(S, device="cuda")[None] < torch.tensor(lens, device="cuda")[:, None]
+    if mask is not None:
+        seen &= mask != 0
+    k[~seen], v[~seen] = float("nan"), float("inf")
+    o = torch.full_like(q, 6.0)
+    st, ln = torch.tensor(starts, dtype=torch.int32, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    abi.hsa_cross_attention(ctx, q, st, n, B, k, v, S, o, kv_len=ln, kv_mask=mask, kv_heads=Hk)
+    abi.hsa_sync_check(ctx)
+    ref, mag = _cross64(q, starts, k, v, lens, mask, H, Hk, d, d ** -0.5)
+    rows = slice(starts[0], starts[-1])
+    _within(o[rows], ref[rows], _cross_tol(ref, mag)[rows])
+    assert bool((o[:5] == 6.0).all()) and bool((o[starts[-1]:] == 6.0).all())
+    for b in range(B):
+        if not bool(seen[b].any()):
+            assert bool((o[starts[b]:starts[b + 1]] == 0).all())
+
+
 def test_cross_attention_layouts_and_scale():
     """Keys and values as halves of one packed projection, sequence-major
     [S, B, ..] states, one sequence shared by all, a scale of the caller's."""

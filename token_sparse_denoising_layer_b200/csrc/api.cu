@@ -129,7 +129,7 @@ bool make_tmap_s8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t co
 
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t depth, uint64_t rows,
                        uint64_t cols, uint64_t row_stride, uint64_t depth_stride,
-                       uint32_t box_rows, std::string* why) {
+                       uint32_t box_rows, std::string* why, uint32_t box_depth) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) {
     if (why) *why = "cuTensorMapEncodeTiled is not available from the driver";
@@ -137,7 +137,7 @@ bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t depth, uint6
   }
   const cuuint64_t dims[3] = {cols, rows, depth};
   const cuuint64_t strides[2] = {row_stride * 2, depth_stride * 2};
-  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t box[3] = {64, box_rows, box_depth};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

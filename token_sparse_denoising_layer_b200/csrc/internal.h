@@ -262,10 +262,10 @@ bool make_tmap_s8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t co
                   uint32_t box_rows, std::string* why);
 
 // TMA descriptor for bf16 matrices [depth][rows, cols] with a box of
-// [1][box_rows, 64] and 128-byte swizzle; strides in elements.
+// [box_depth][box_rows, 64] and 128-byte swizzle; strides in elements.
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t depth, uint64_t rows,
                        uint64_t cols, uint64_t row_stride, uint64_t depth_stride,
-                       uint32_t box_rows, std::string* why);
+                       uint32_t box_rows, std::string* why, uint32_t box_depth = 1);
 
 // TMA descriptor for a row-major bf16 matrix [rows, cols] with a
 // box of [box_rows, 64] and 128-byte swizzle.  Returns false on failure.

@@ -6,19 +6,22 @@
 // row m, over the keys j < kv_len[b] whose mask byte is set.
 //
 // Arithmetic of a tile as in the active-query attention (k_attn.cu): two
-// 128-query tiles of one head share every 128-key tile, S and O live in TMEM,
+// tiles of 128 rows share every 128-key tile, S and O live in TMEM,
 // P is written over S as bf16 and read from there by the second product, and
 // the two query tiles ping-pong.  What differs:
-//  - One persistent CTA per SM walks over units of 256 queries x one head.  Key
+//  - A row is a query and a head: where several query heads share a key head, a
+//    power of two of them may lie side by side in a tile (launch_hd says when),
+//    so that short sequences fill it.
+//  - One persistent CTA per SM walks over units of 256 rows.  Key
 //    sets are short (a prompt is a few tiles), so a CTA per unit spent two
 //    thirds of its time on its own start and end: the next unit's descriptor, Q
 //    and first keys now arrive while this one's last tile is in softmax, and
 //    its first scores are computed under this one's epilogue.  (26207 queries,
-//    12 heads x 128, 512 and 384 keys: 145 us with a CTA per unit, 91 now.)
+//    12 heads x 128, 512 and 384 keys: 145 us with a CTA per unit, 93 now.)
 //  - Which rows and keys a unit covers is read on the device.  Units are
-//    numbered per head so that sequence b's first one is
-//    floor(q_start[b] / 256) + b: every sequence has room for its last,
-//    partial unit, the host knows their number (n / 256 + B) without knowing
+//    numbered per head (or packed heads) so that sequence b's first one is
+//    floor(its first row / 256) + b: every sequence has room for its last,
+//    partial unit, the host knows their number (rows / 256 + B) without knowing
 //    the lengths, and a unit's sequence is found by a search over q_start
 //    alone.  The producer warp finds the next unit that has rows and passes
 //    its descriptor to the other warps through a ring of two.
@@ -36,6 +39,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -49,8 +53,9 @@ namespace hsa {
 
 namespace {
 
-constexpr int kQ = 128;        // queries per tile
-constexpr int kUnitQ = 2 * kQ; // queries per unit
+constexpr int kQ = 128;        // rows (queries x packed heads) per tile
+constexpr int kUnitQ = 2 * kQ; // rows per unit
+constexpr int kMaxPack = 32;   // a warp's 32 rows are whole queries
 constexpr int kStages = 2;     // K and V ring depth
 constexpr int kThreads = 320;
 constexpr int kSoftmaxWarps = 8;
@@ -75,7 +80,7 @@ static_assert(CrossCfg<64>::kBarsAt + 1024 + 512 <= CrossCfg<64>::kSmem &&
 // What the warps of a CTA need to know of a unit (or of one key range of it).
 struct UnitDesc {
   int q0, q1;    // rows
-  int b, h;      // sequence, query head
+  int b, h;      // sequence, group of packed query heads
   int j0, nkv;   // key tiles [j0, j0 + nkv); nkv < 0: no more units
   int len;       // keys of the sequence
   int part;      // index of this key range's partial result, or -1
@@ -91,7 +96,9 @@ struct CrossParams {
   const int32_t* kv_len;
   const uint8_t* kv_mask;
   int* flag;
-  // Work: units_per_head * H units, each in `split` key ranges; with more than
+  // Row r of head group h is query r >> pack of head (h << pack) + r mod 2^pack.
+  int pack;
+  // Work: units_per_head * (H >> pack) units, each in `split` key ranges; with more than
   // one, partial results are merged by k_cross_combine.
   int units_per_head, units, split;
   float* part_o;
@@ -102,7 +109,14 @@ __device__ __forceinline__ int clamped(int v, int lo, int hi) { return v < lo ? 
 
 // First row of sequence b's queries (b = B: one past the last row).
 __device__ __forceinline__ int first_row(const CrossParams& p, int b) {
-  return p.q_start != nullptr ? clamped(__ldg(p.q_start + b), 0, p.n) : b * (p.n / p.B);
+  return (p.q_start != nullptr ? clamped(__ldg(p.q_start + b), 0, p.n) : b * (p.n / p.B)) << p.pack;
+}
+
+// Where row r of head group h starts in o.
+template <int HD>
+__device__ __forceinline__ __nv_bfloat16* out_row(const CrossParams& p, int h, int r) {
+  const int head = (h << p.pack) + (r & ((1 << p.pack) - 1));
+  return p.o + static_cast<size_t>(r >> p.pack) * p.ld + head * HD;
 }
 
 // Sequence and rows [q0, q1) of unit u of a head, by a 32-way search over the
@@ -275,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int ntile = d.q0 + kQ < d.q1 ? 2 : 1;
         const int bk = p.k_shared ? 0 : d.b, bv = p.v_shared ? 0 : d.b;
-        const int qcol = d.h * HD, kcol = d.h / p.group * HD;
+        const int head = d.h << p.pack, kcol = head / p.group * HD;
         for (int j = 0; j < d.nkv && ok; ++j, ++it) {
           const int s = it % kStages;
           const uint32_t ph = ((it / kStages) & 1) ^ 1;
@@ -298,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(q_full, ntile * Cfg::kTileBytes);
             for (int t = 0; t < ntile; ++t)
               for (int r = 0; r < Cfg::kRegions; ++r)
-                tma_load_2d(sQ + t * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmQ, q_full,
-                            qcol + 64 * r, d.q0 + t * kQ);
+                tma_load_3d(sQ + t * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmQ, q_full, 64 * r, head,
+                            (d.q0 + t * kQ) >> p.pack);
           }
           if (!mbar_wait(&v_empty[s], ph)) {
             (void)mbar_wait(&k_full[s], (it / kStages) & 1);
@@ -440,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           for (int r = 0; r < rows; ++r)
             if (lane < HD / 8)
-              *reinterpret_cast<uint4*>(p.o + static_cast<size_t>(warp_row + r) * p.ld + d.h * HD + 8 * lane) =
+              *reinterpret_cast<uint4*>(out_row<HD>(p, d.h, warp_row + r) + 8 * lane) =
                   make_uint4(0u, 0u, 0u, 0u);
         }
         continue;
@@ -599,19 +613,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&tmO, stage, d.h * HD + 32 * (c - 1), warp_row);
+              tma_store_3d(&tmO, stage, 32 * (c - 1), d.h << p.pack, warp_row >> p.pack);
               tma_store_commit();
             }
           } else {
             // the next rows are another sequence's: one store covers four rows
             // and 128 contiguous bytes of each
             __syncwarp();
-            __nv_bfloat16* dst = p.o + static_cast<size_t>(warp_row) * p.ld + d.h * HD + 32 * (c - 1) + 8 * g;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int rr = 4 * k + (lane >> 3);
               if (warp_row + rr < d.q1)
-                *reinterpret_cast<uint4*>(dst + static_cast<size_t>(rr) * p.ld) =
+                *reinterpret_cast<uint4*>(out_row<HD>(p, d.h, warp_row + rr) + 32 * (c - 1) + 8 * g) =
                     *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
             }
             __syncwarp();
@@ -661,7 +674,7 @@ __global__ void __launch_bounds__(256) k_cross_combine(const __grid_constant__ C
     for (int c = 0; c < kPer; ++c) acc[c] += po[lane + 32 * c] * wgt;
   }
   const float inv = L == 0.f ? 0.f : 1.0f / L;
-  __nv_bfloat16* orow = p.o + static_cast<size_t>(q0 + rr) * p.ld + h * HD;
+  __nv_bfloat16* orow = out_row<HD>(p, h, q0 + rr);
 #pragma unroll
   for (int c = 0; c < kPer; ++c) orow[lane + 32 * c] = __float2bfloat16_rn(acc[c] * inv);
 }
@@ -671,18 +684,49 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
   const int D = c.cfg.D, H = c.cfg.H;
   const bool k1 = a.B == 1 || a.bs_k == 0, v1 = a.B == 1 || a.bs_v == 0;
   const uint64_t width = static_cast<uint64_t>(a.kv_heads) * HD;
-  CUtensorMap tq, tk, tv, to;
-  if (!make_tmap_bf16(&tq, a.q, a.n, D, D, kQ, why)) return cudaErrorInvalidValue;
-  if (!make_tmap_bf16_3d(&tk, a.k, k1 ? 1 : a.B, a.S, width, a.ld_k, k1 ? a.ld_k * a.S : a.bs_k, kKV, why))
-    return cudaErrorInvalidValue;
-  if (!make_tmap_bf16_3d(&tv, a.v, v1 ? 1 : a.B, a.S, width, a.ld_v, v1 ? a.ld_v * a.S : a.bs_v, kKV, why))
-    return cudaErrorInvalidValue;
-  if (!make_tmap_bf16(&to, a.o, a.n, D, D, 32, why)) return cudaErrorInvalidValue;
   CrossParams p{};
   p.n = a.n;
   p.B = a.B;
   p.S = a.S;
   p.group = H / a.kv_heads;
+  // Packed heads and key ranges per unit: the rounds of CTAs times the tiles of a
+  // range, plus two tiles' time for a unit's own ends and six for the merge,
+  // whichever is least.  Packing the query heads of a key head fills the tiles
+  // of short sequences; where it saves no round, heads of their own load less
+  // at once (100 queries, 24 heads of 4 key heads x 128, 512 keys: 12.7 us
+  // against 14.5 with two heads a tile; 8 sequences of two queries, 32 heads of 2,
+  // 4096 keys: 17.4 us against 105.6 without).
+  const int tiles = (a.S + kKV - 1) / kKV;
+  constexpr int kMaxUnits = 0x3fffffff / kMaxSplitParts;
+  int64_t best = INT64_MAX;
+  for (int pack = 0; (1 << pack) <= kMaxPack && p.group % (1 << pack) == 0; ++pack) {
+    const int64_t rows = static_cast<int64_t>(a.n) << pack;
+    const int64_t units64 = (rows / kUnitQ + a.B) * (H >> pack);
+    if (rows > INT_MAX || units64 > kMaxUnits) continue;
+    const int units = static_cast<int>(units64);
+    for (int sp = 1; sp <= tiles && sp <= kMaxSplitParts && (sp == 1 || units * sp <= kMaxAttnParts); ++sp) {
+      const int rounds = (units * sp + c.num_sms - 1) / c.num_sms;
+      const int64_t cost = static_cast<int64_t>(rounds) * ((tiles + sp - 1) / sp + 2) + (sp > 1 ? 6 : 0);
+      if (cost >= best) continue;
+      best = cost;
+      p.units = units;
+      p.units_per_head = units / (H >> pack);
+      p.pack = pack;
+      p.split = sp;
+    }
+  }
+  if (p.units == 0) {
+    if (why) *why = "too many sequences";
+    return cudaErrorInvalidValue;
+  }
+  const uint32_t heads = 1u << p.pack;  // Q and O as [queries][heads][columns]
+  CUtensorMap tq, tk, tv, to;
+  if (!make_tmap_bf16_3d(&tq, a.q, a.n, H, HD, HD, D, heads, why, kQ / heads)) return cudaErrorInvalidValue;
+  if (!make_tmap_bf16_3d(&tk, a.k, k1 ? 1 : a.B, a.S, width, a.ld_k, k1 ? a.ld_k * a.S : a.bs_k, kKV, why))
+    return cudaErrorInvalidValue;
+  if (!make_tmap_bf16_3d(&tv, a.v, v1 ? 1 : a.B, a.S, width, a.ld_v, v1 ? a.ld_v * a.S : a.bs_v, kKV, why))
+    return cudaErrorInvalidValue;
+  if (!make_tmap_bf16_3d(&to, a.o, a.n, H, HD, HD, D, heads, why, 32 / heads)) return cudaErrorInvalidValue;
   p.k_shared = k1;
   p.v_shared = v1;
   const double scale = a.scale != 0.f ? a.scale : 1.0 / sqrt(static_cast<double>(HD));
@@ -701,26 +745,9 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
                                : ensure_smem_limit(k_cross<HD, false>, smem, c.device, smem_set[0]);
     if (e != cudaSuccess) return e;
   }
-  p.units_per_head = a.n / kUnitQ + a.B;
-  const int64_t units64 = static_cast<int64_t>(p.units_per_head) * H;
-  if (units64 > 0x3fffffff / kMaxSplitParts) {
-    if (why) *why = "too many sequences";
-    return cudaErrorInvalidValue;
-  }
-  p.units = static_cast<int>(units64);
-  // Key ranges per unit: the rounds of CTAs times the tiles of a range, plus two
-  // tiles' time for a unit's own ends and six for the merge, whichever is least.
-  const int tiles = (a.S + kKV - 1) / kKV;
-  auto cost = [&](int sp) {
-    const int64_t rounds = (units64 * sp + c.num_sms - 1) / c.num_sms;
-    return rounds * ((tiles + sp - 1) / sp + 2) + (sp > 1 ? 6 : 0);
-  };
-  p.split = 1;
-  for (int sp = 2; sp <= tiles && sp <= kMaxSplitParts && units64 * sp <= kMaxAttnParts; ++sp)
-    if (cost(sp) < cost(p.split)) p.split = sp;
   p.part_o = c.attn_part_o;
   p.part_ml = reinterpret_cast<float2*>(c.attn_part_ml);
-  const int64_t items = units64 * p.split;
+  const int items = p.units * p.split;
   const unsigned grid = static_cast<unsigned>(items < c.num_sms ? items : c.num_sms);
   if (mask) k_cross<HD, true><<<grid, kThreads, smem, c.stream>>>(tq, tk, tv, to, p);
   else k_cross<HD, false><<<grid, kThreads, smem, c.stream>>>(tq, tk, tv, to, p);
