@@ -535,6 +535,8 @@ def test_cross_attention_rows_of_no_sequence_are_left():
     (32, 1, 64, 9, 32, 77, 0),
     (64, 1, 64, 40, 8, 1000, 0.9),  # more heads than are packed
     (32, 2, 128, 2, 8, 4096, 0),    # and key ranges that are merged
+    (24, 24, 64, 23, 13, 1389, 0),  # nothing to pack: a lone tile a unit
+    (4, 4, 128, 120, 9, 700, 0.3),
 ])
 def test_cross_attention_packs_the_heads_of_a_key_head(H, Hk, d, step, B, S, holes):
     need_gpu()

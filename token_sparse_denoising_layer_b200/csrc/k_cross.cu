@@ -17,7 +17,7 @@
 //    thirds of its time on its own start and end: the next unit's descriptor, Q
 //    and first keys now arrive while this one's last tile is in softmax, and
 //    its first scores are computed under this one's epilogue.  (26207 queries,
-//    12 heads x 128, 512 and 384 keys: 145 us with a CTA per unit, 93 now.)
+//    12 heads x 128, 512 and 384 keys: 145 us with a CTA per unit, 91 now.)
 //  - Which rows and keys a unit covers is read on the device.  Units are
 //    numbered per head (or packed heads) so that sequence b's first one is
 //    floor(its first row / 256) + b: every sequence has room for its last,
@@ -71,7 +71,7 @@ struct CrossCfg {
   static constexpr int kBarsAt = kStageAt + kSoftmaxWarps * kStageBytes;
   // Every CTA takes all 512 TMEM columns, so only one may be resident per SM.
   static constexpr int kSmem = HD == 64 ? 160 * 1024 : kBarsAt + 1024 + 512;
-  static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + HD;
+  static constexpr uint32_t kColS = 0, kColO = 2 * kKV;  // two S tiles (P over S), two O tiles
 };
 static_assert(CrossCfg<64>::kBarsAt + 1024 + 512 <= CrossCfg<64>::kSmem &&
                   CrossCfg<128>::kSmem <= 227 * 1024,
@@ -214,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_empty = k_full + kStages;
   uint64_t* v_full = k_empty + kStages;
   uint64_t* v_empty = v_full + kStages;
-  uint64_t* s_full = v_empty + kStages;  // [2] per query tile
-  uint64_t* p_full = s_full + 2;         // [2]
-  uint64_t* o_done = p_full + 2;         // [2]
+  uint64_t* s_full = v_empty + kStages;  // [2][2] per query tile, its S tiles in turn
+  uint64_t* p_full = s_full + 4;         // [2][2]
+  uint64_t* o_done = p_full + 4;         // [2] per query tile
   uint64_t* d_full = o_done + 2;         // [2] descriptors
   uint64_t* d_empty = d_full + 2;        // [2]
   UnitDesc* desc = reinterpret_cast<UnitDesc*>(d_empty + 2);  // [2]
@@ -224,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // a barrier per lane: q_full .. v_empty, s_full, p_full, o_done, d_full, d_empty
-  constexpr int kP = 4 * kStages + 4, kD = kP + 6;  // first of p_full and of d_empty
+  constexpr int kP = 6 + 4 * kStages, kD = kP + 8;  // first of p_full and of d_empty
   if (warp == 0 && lane < kD + 2) {
-    mbar_init(bars + lane, lane >= kD ? 1 + kSoftmaxWarps : lane >= kP && lane < kP + 2 ? 4 : 1);
+    mbar_init(bars + lane, lane >= kD ? 1 + kSoftmaxWarps : lane >= kP && lane < kP + 4 ? 4 : 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -342,26 +342,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idS = idesc_bf16(kQ, kKV, false, false);
       constexpr uint32_t idPV = idesc_bf16(kQ, HD, false, true);
-      auto issue_s = [&](int t, int s) {
-        const uint32_t q_addr = smem_u32(sQ + t * Cfg::kTileBytes);
-        const uint32_t k_addr = smem_u32(sK + s * Cfg::kTileBytes);
+      // This thread's own work shows: descriptors are one sum each (their low bits
+      // are addresses / 16), and the tile index is known to the compiler (26207
+      // queries, 12 heads x 128: 90.6 us; 91.6 with descriptors built for each
+      // instruction, 99 with the tile index in a register as well).
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024), k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(sV), Cfg::kRegionBytes, 1024);
+      auto issue_s = [&](int t, int s, int buf) {
+        const uint64_t a = q_desc + t * (Cfg::kTileBytes >> 4), b = k_desc + s * (Cfg::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * Cfg::kRegionBytes + (kk & 3) * 32;
-          umma_bf16(tmem + (t == 0 ? Cfg::kColS0 : Cfg::kColS1), sdesc_sw128(q_addr + off, 16, 1024),
-                    sdesc_sw128(k_addr + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+          const int off = ((kk >> 2) * Cfg::kRegionBytes + (kk & 3) * 32) >> 4;
+          umma_bf16(tmem + Cfg::kColS + buf * kKV, a + off, b + off, idS, kk > 0 ? 1u : 0u);
         }
       };
-      auto issue_pv = [&](int t, int s, bool acc) {
-        const uint32_t v_addr = smem_u32(sV + s * Cfg::kTileBytes);
+      auto issue_pv = [&](int t, int s, int buf, bool acc) {
+        const uint64_t b = v_desc + s * (Cfg::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kKV / 16; ++kk)
-          umma_bf16_ta(tmem + (t == 0 ? Cfg::kColO0 : Cfg::kColO1),
-                       tmem + (t == 0 ? Cfg::kColS0 : Cfg::kColS1) + kk * 8,
-                       sdesc_sw128(v_addr + kk * 2048, Cfg::kRegionBytes, 1024), idPV,
-                       (acc || kk > 0) ? 1u : 0u);
+          umma_bf16_ta(tmem + Cfg::kColO + t * HD, tmem + Cfg::kColS + buf * kKV + kk * 8,
+                       b + kk * (2048 >> 4), idPV, (acc || kk > 0) ? 1u : 0u);
       };
-      int it = 0, nq = 0, np0 = 0, np1 = 0;  // key tiles, units with keys, P tiles of either query tile
+      int it = 0, nq = 0;  // key tiles (also: S tiles of query tile 0), units with keys
+      int n1 = 0;          // S tiles of query tile 1
       for (int nd = 0;; ++nd) {
         if (!mbar_wait(&d_full[nd & 1], (nd >> 1) & 1)) {
           ok = false;
@@ -372,49 +375,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&d_empty[nd & 1]);
         if (nkv < 0) break;
         if (nkv == 0) continue;
-        ok = mbar_wait(q_full, nq & 1) && mbar_wait(&k_full[it % kStages], (it / kStages) & 1);
+        ok = mbar_wait(q_full, nq & 1);
         if (!ok) break;
         ++nq;
-        tc_fence_after();
-        for (int t = 0; t < ntile; ++t) {
-          issue_s(t, it % kStages);
-          umma_commit(&s_full[t]);
+        auto scores = [&](int t, int j, int buf) {
+          const int s = (it + j) % kStages, nth = (t == 0 ? it : n1) + j;
+          if (t == 0 && !mbar_wait(&k_full[s], ((it + j) / kStages) & 1)) return false;
+          tc_fence_after();
+          issue_s(t, s, buf);
+          umma_commit(&s_full[2 * t + (nth & 1)]);
+          if (t == ntile - 1) umma_commit(&k_empty[s]);
+          if (t == ntile - 1 && j == nkv - 1) umma_commit(q_empty);
+          return true;
+        };
+        auto values = [&](int t, int j, int buf) {
+          const int s = (it + j) % kStages, nth = (t == 0 ? it : n1) + j;
+          // p_full of query tile 0 also says that the unseen rows of this V tile are zeroed
+          if (!mbar_wait(&p_full[2 * t + (nth & 1)], (nth >> 1) & 1)) return false;
+          if (t == 0 && !mbar_wait(&v_full[s], ((it + j) / kStages) & 1)) return false;
+          tc_fence_after();
+          issue_pv(t, s, buf, j > 0);
+          if (t == ntile - 1) umma_commit(&v_empty[s]);
+          if (j == nkv - 1) umma_commit(&o_done[t]);
+          return true;
+        };
+        // Scores follow the P V that leaves their buffer: the tensor pipe works in
+        // order, so that product has read P by then.
+        if (ntile == 2) {  // a buffer each
+          ok = scores(0, 0, 0) && scores(1, 0, 1);
+          for (int j = 0; j < nkv && ok; ++j)
+#pragma unroll
+            for (int t = 0; t < 2 && ok; ++t) ok = values(t, j, t) && (j + 1 == nkv || scores(t, j + 1, t));
+          n1 += nkv;
+        } else {
+          // A lone query tile takes both in turn: its next scores are computed under
+          // its softmax (100 queries, 12 heads x 128, 512 keys: 12.3 us with one
+          // buffer, 10.6 with both).
+          ok = scores(0, 0, 0) && (nkv == 1 || scores(0, 1, 1));
+          for (int j = 0; j < nkv && ok; ++j) ok = values(0, j, j & 1) && (j + 2 >= nkv || scores(0, j + 2, j & 1));
         }
-        umma_commit(&k_empty[it % kStages]);
-        if (nkv == 1) umma_commit(q_empty);
-        for (int j = 0; j < nkv && ok; ++j, ++it) {
-          const int s = it % kStages;
-          const int s1 = (it + 1) % kStages;
-          for (int t = 0; t < ntile && ok; ++t) {
-            // p_full[0] also says that the unseen rows of this V tile are zeroed
-            if (!mbar_wait(&p_full[t], (t == 0 ? np0++ : np1++) & 1)) {
-              ok = false;
-              break;
-            }
-            if (t == 0 && !mbar_wait(&v_full[s], (it / kStages) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            issue_pv(t, s, j > 0);
-            if (t == ntile - 1) umma_commit(&v_empty[s]);
-            if (j + 1 < nkv) {
-              if (t == 0 && !mbar_wait(&k_full[s1], ((it + 1) / kStages) & 1)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              issue_s(t, s1);
-              umma_commit(&s_full[t]);
-              if (t == ntile - 1) {
-                umma_commit(&k_empty[s1]);
-                if (j + 2 == nkv) umma_commit(q_empty);
-              }
-            } else {
-              umma_commit(&o_done[t]);
-            }
-          }
-        }
+        it += nkv;
         if (!ok) break;
       }
     }
@@ -424,8 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qd = warp & 3;        // TMEM lane quarter
     const int row = 32 * qd + lane;
     const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
-    const uint32_t tS = tmem + lane_base + (t == 0 ? Cfg::kColS0 : Cfg::kColS1);
-    const uint32_t tO = tmem + lane_base + (t == 0 ? Cfg::kColO0 : Cfg::kColO1);
+    const uint32_t tO = tmem + lane_base + Cfg::kColO + t * HD;
     uint8_t* stage = smem + Cfg::kStageAt + (warp - 2) * kStageBytes;
     if (blockIdx.x == 0) {  // while nothing has arrived yet, one CTA looks the offsets and lengths over
       for (int i = threadIdx.x - 64; i < p.B; i += 32 * kSoftmaxWarps) {
@@ -459,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      if (t == 1 && d.q0 + kQ >= d.q1) {  // no second query tile
+      const int ntile = d.q0 + kQ < d.q1 ? 2 : 1;
+      if (t >= ntile) {
         it += d.nkv;
         continue;
       }
@@ -507,11 +507,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           first_bits(d.len - (d.j0 + j) * kKV, see);
         }
         const bool whole = (see[0] & see[1] & see[2] & see[3]) == 0xffffffffu;  // same for all rows
-        if (!clear_unseen(see)) {
-          ok = false;
-          break;
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], ns & 1))) {
+        const uint32_t tS = tmem + lane_base + Cfg::kColS + ((ntile == 2 ? t : j) & 1) * kKV;
+        // A lone query tile may be two tiles ahead of P V: only its scores say then that
+        // the load before has reached the stage, and so which phase its barrier is in.
+        const auto scored = [&] {
+          return __all_sync(0xffffffffu, mbar_wait(&s_full[2 * t + (ns & 1)], (ns >> 1) & 1)) != 0;
+        };
+        if ((ntile == 1 && j >= 2 && !scored()) || !clear_unseen(see) || !scored()) {
           ok = false;
           break;
         }
@@ -533,6 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             rs = exp_row(sr, p.scale_log2, m_use, w);
             const bool over = !(rs <= kSumLimit);
             if (j == 0 || pass == 1 || !__any_sync(0xffffffffu, over)) break;
+            // a lone query tile's last P V may still be adding to O (the one before is
+            // done: it was issued ahead of these scores)
+            if (ntile == 1 &&
+                !__all_sync(0xffffffffu, mbar_wait(&v_empty[(it - 1) % kStages], ((it - 1) / kStages) & 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
             tmem_ld128(tS, sr);
             if (!whole) hide(sr, see);
             const float tmax = row_max(sr) * p.scale_log2;
@@ -555,9 +565,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run = l_run * alpha + rs;
           m_run = m_use;
         }
+        if (!ok) break;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        if (lane == 0) mbar_arrive(&p_full[2 * t + (ns & 1)]);
       }
       if (!ok) break;
       // epilogue: O / l -> bf16 rows through this warp's stage, or, for a
