@@ -5,19 +5,21 @@
 // Every key and value is read once for up to kFewRows rows that share it (the queries of
 // a sequence times the query heads of a key head), so what bounds this is HBM
 // and, before that, the bytes in flight.  A lane group of d / 8 lanes owns a
-// key: 16 bytes of K and of V a lane, kBatch keys loaded together.  Scores are
+// key: 16 bytes of K and of V a lane, kBatch keys at a time.  Scores are
 // summed over the group by shuffles; each group keeps its own running maximum,
 // sum and output in fp32 (weights are never rounded to 16 bits here), and these are
 // merged over the groups of a warp by shuffles, over the warps of a CTA in shared
 // memory and over the CTAs of a cluster, which split the keys when there are
 // few sequences, through distributed shared memory.  16 sequences of one query,
-// 12 heads x 128, up to 512 keys: 12 us (24 in 128-query tiles; the bytes alone take 5.5).
+// 12 heads x 128, up to 512 keys: 11.5 us (24 in 128-query tiles; the bytes alone take 5.5).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -26,7 +28,7 @@ namespace hsa {
 
 namespace {
 
-constexpr int kBatch = 4;    // keys of a lane group loaded together
+constexpr int kBatch = 4;    // keys of a lane group at a time
 constexpr int kFewRows = 4;  // rows of one pass over the keys
 
 // Warps of a CTA: four rows' states fill the registers of half as many threads
@@ -34,6 +36,15 @@ constexpr int kFewRows = 4;  // rows of one pass over the keys
 template <int R>
 constexpr int warps_of() {
   return R == kFewRows ? 4 : 8;
+}
+
+// With more rows than one, few warps fit an SM and the next batch is on its way into
+// shared memory while one is used (16 sequences, 2 rows a key head, 1024 keys: 24.1 us
+// against 26.9, 4 rows, 2000 keys: 14.6 against 16.5).  One row's threads have their batch in
+// registers: three CTAs an SM cover for one another (tokens as above: 11.5 us, 12.4 with the ring).
+template <int R>
+constexpr int ring_bytes() {
+  return R == 1 ? 0 : 2 * kBatch * 2 * 16 * 32 * warps_of<R>();
 }
 
 struct FewParams {
@@ -82,6 +93,8 @@ __global__ void __launch_bounds__(32 * warps_of<R>(), R == 1 ? 3 : 2)
   __shared__ __align__(16) float s_o[kWarps][R][HD];
   __shared__ float c_ml[R][2];
   __shared__ __align__(16) float c_o[R][HD];
+  constexpr bool kRing = ring_bytes<R>() > 0;
+  extern __shared__ __align__(16) uint4 ring[];  // [2][kBatch][K, V][thread]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane / L, e = 8 * (lane % L);  // key of the warp's step, first place of this lane
 
@@ -106,6 +119,27 @@ __global__ void __launch_bounds__(32 * warps_of<R>(), R == 1 ? 3 : 2)
   const int first = min(len, rank * per), last = min(len, first + per);
 
   for (int r0 = 0; r0 < rows; r0 += R) {
+    // A thread copies and reads its own places only, so the ring has no barriers.
+    auto place = [&](int stage, int u, int kv) -> uint4& {
+      return ring[((stage * kBatch + u) * 2 + kv) * (32 * kWarps) + threadIdx.x];
+    };
+    uint8_t ahead[kBatch];  // whether the keys on their way are seen
+    auto fetch = [&](int j0, int stage) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int j = j0 + u * G + g;
+        ahead[u] = 0;
+        if (j < last) {
+          cp_async16(&place(stage, u, 0), kb + j * p.ld_k);
+          cp_async16(&place(stage, u, 1), vb + j * p.ld_v);
+          ahead[u] = mask != nullptr ? __ldg(mask + j) : 1;
+        }
+      }
+      cp_async_commit();
+    };
+    constexpr int kStep = kWarps * G * kBatch;
+    int stage = 0;
+    if (kRing) fetch(first + warp * G * kBatch, 0);
     float qf[R][8];
     Run run[R];
 #pragma unroll
@@ -120,18 +154,27 @@ __global__ void __launch_bounds__(32 * warps_of<R>(), R == 1 ? 3 : 2)
       run[r].m = -FLT_MAX;
       run[r].l = 0.f;
     }
-    for (int j0 = first + warp * G * kBatch; j0 < last; j0 += kWarps * G * kBatch) {
+    for (int j0 = first + warp * G * kBatch; j0 < last; j0 += kStep, stage ^= 1) {
       uint4 kr[kBatch], vr[kBatch];
       bool see[kBatch];
+      if (kRing) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int j = j0 + u * G + g;
-        see[u] = j < last;
-        kr[u] = vr[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (see[u]) {
-          kr[u] = __ldg(reinterpret_cast<const uint4*>(kb + j * p.ld_k));
-          vr[u] = __ldg(reinterpret_cast<const uint4*>(vb + j * p.ld_v));
-          if (mask != nullptr) see[u] = __ldg(mask + j) != 0;
+        for (int u = 0; u < kBatch; ++u) see[u] = ahead[u] != 0;
+        fetch(j0 + kStep, stage ^ 1);
+        cp_async_wait<1>();
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) kr[u] = place(stage, u, 0), vr[u] = place(stage, u, 1);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int j = j0 + u * G + g;
+          see[u] = j < last;
+          kr[u] = vr[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (see[u]) {
+            kr[u] = __ldg(reinterpret_cast<const uint4*>(kb + j * p.ld_k));
+            vr[u] = __ldg(reinterpret_cast<const uint4*>(vb + j * p.ld_v));
+            if (mask != nullptr) see[u] = __ldg(mask + j) != 0;
+          }
         }
       }
 #pragma unroll
@@ -185,6 +228,7 @@ __global__ void __launch_bounds__(32 * warps_of<R>(), R == 1 ? 3 : 2)
           for (int i = 0; i < 8; ++i) run[r].o[i] = fmaf(s[r][u], vf[i], run[r].o[i]);
       }
     }
+    if (kRing) cp_async_wait<0>();
     // the lane groups of the warp
 #pragma unroll
     for (int o = L; o < 32; o <<= 1)
@@ -269,7 +313,12 @@ __global__ void __launch_bounds__(32 * warps_of<R>(), R == 1 ? 3 : 2)
 
 template <int HD, int R>
 cudaError_t launch_rows(const Ctx& c, const FewParams& p) {
+  constexpr int smem = ring_bytes<R>();
+  static std::atomic<uint64_t> smem_set = {};  // per device
+  cudaError_t e = smem > 0 ? ensure_smem_limit(k_cross_few<HD, R>, smem, c.device, smem_set) : cudaSuccess;
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.kv_heads * p.split);
   cfg.blockDim = dim3(32 * warps_of<R>());
   cfg.stream = c.stream;
@@ -279,7 +328,7 @@ cudaError_t launch_rows(const Ctx& c, const FewParams& p) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_cross_few<HD, R>, p);
+  e = cudaLaunchKernelEx(&cfg, k_cross_few<HD, R>, p);
   c.launches += 1;
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -289,9 +338,9 @@ cudaError_t launch_rows(const Ctx& c, const FewParams& p) {
 cudaError_t launch_cross_few(const Ctx& c, const hsa_cross_args& a, bool* taken) {
   const int H = c.cfg.H, hd = c.cfg.D / H, group = H / a.kv_heads;
   const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads;
-  // One pass over the keys for a sequence of average length.  With more rows a
-  // 128-query tile is faster although most of it is empty (16 sequences: 4 rows a key head,
-  // 2000 keys 17 us here and 40 in tiles; 6 rows, 512 keys 55 and 23).
+  // One pass over the keys for a sequence of average length.  With more rows the
+  // 128-row tiles are as fast (16 sequences, 2 key heads, 2000 keys: 4 rows a key
+  // head 14.3 us here, 8 rows 15.4 there).
   const int64_t rows = static_cast<int64_t>(a.n) * group;
   *taken = rows <= static_cast<int64_t>(a.B) * kFewRows && items * 8 < 0x7fffffff;
   if (!*taken) return cudaSuccess;
