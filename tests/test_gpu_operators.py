@@ -535,6 +535,10 @@ def test_cross_attention_rows_of_no_sequence_are_left():
     (32, 1, 64, 9, 32, 77, 0),
     (64, 1, 64, 40, 8, 1000, 0.9),  # more heads than are packed
     (32, 2, 128, 2, 8, 4096, 0),    # and key ranges that are merged
+    (40, 8, 64, 3, 16, 300, 0),     # five heads a query, 125 of a tile's 128 rows
+    (28, 4, 64, 17, 30, 200, 0.4),  # seven
+    (20, 1, 64, 70, 3, 2500, 0),    # twenty, six queries a tile, merged key ranges
+    (12, 4, 128, 33, 30, 140, 0.1),
     (24, 24, 64, 23, 13, 1389, 0),  # nothing to pack: a lone tile a unit
     (4, 4, 128, 120, 9, 700, 0.3),
 ])

@@ -9,10 +9,10 @@
 // tiles of 128 rows share every 128-key tile, S and O live in TMEM,
 // P is written over S as bf16 and read from there by the second product, and
 // the two query tiles ping-pong.  What differs:
-//  - A row is a query and a head: where several query heads share a key head, a
-//    power of two of them may lie side by side in a tile (launch_hd says when),
-//    so that short sequences fill it.
-//  - One persistent CTA per SM walks over units of 256 rows.  Key
+//  - A row is a query and a head: where several query heads share a key head, some
+//    of them may lie side by side in a tile (launch_hd says when), so that short
+//    sequences fill it.
+//  - One persistent CTA per SM walks over units of two tiles.  Key
 //    sets are short (a prompt is a few tiles), so a CTA per unit spent two
 //    thirds of its time on its own start and end: the next unit's descriptor, Q
 //    and first keys now arrive while this one's last tile is in softmax, and
@@ -20,8 +20,8 @@
 //    12 heads x 128, 512 and 384 keys: 145 us with a CTA per unit, 91 now.)
 //  - Which rows and keys a unit covers is read on the device.  Units are
 //    numbered per head (or packed heads) so that sequence b's first one is
-//    floor(its first row / 256) + b: every sequence has room for its last,
-//    partial unit, the host knows their number (rows / 256 + B) without knowing
+//    floor(its first query / a unit's queries) + b: every sequence has room for its last,
+//    partial unit, the host knows their number without knowing
 //    the lengths, and a unit's sequence is found by a search over q_start
 //    alone.  The producer warp finds the next unit that has rows and passes
 //    its descriptor to the other warps through a ring of two.
@@ -39,7 +39,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
-#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -53,9 +52,8 @@ namespace hsa {
 
 namespace {
 
-constexpr int kQ = 128;        // rows (queries x packed heads) per tile
-constexpr int kUnitQ = 2 * kQ; // rows per unit
-constexpr int kMaxPack = 32;   // a warp's 32 rows are whole queries
+constexpr int kQ = 128;        // rows (queries x packed heads) a tile has room for
+constexpr int kMaxPack = 32;   // query heads side by side in a tile, at most
 constexpr int kStages = 2;     // K and V ring depth
 constexpr int kThreads = 320;
 constexpr int kSoftmaxWarps = 8;
@@ -79,7 +77,7 @@ static_assert(CrossCfg<64>::kBarsAt + 1024 + 512 <= CrossCfg<64>::kSmem &&
 
 // What the warps of a CTA need to know of a unit (or of one key range of it).
 struct UnitDesc {
-  int q0, q1;    // rows
+  int q0, rows;  // first query, rows
   int b, h;      // sequence, group of packed query heads
   int j0, nkv;   // key tiles [j0, j0 + nkv); nkv < 0: no more units
   int len;       // keys of the sequence
@@ -96,9 +94,12 @@ struct CrossParams {
   const int32_t* kv_len;
   const uint8_t* kv_mask;
   int* flag;
-  // Row r of head group h is query r >> pack of head (h << pack) + r mod 2^pack.
-  int pack;
-  // Work: units_per_head * (H >> pack) units, each in `split` key ranges; with more than
+  // Row r of head group h is query r / pack of head h * pack + r % pack.  A tile has
+  // whole queries, tile_q of them in `tile` rows, a unit twice as many.
+  int pack, tile_q, tile, unit_q;
+  uint32_t over_pack;             // 65536 / pack, rounded up: divides what is below 256
+  uint32_t over_unit, unit_shift;  // 2^(32 + unit_shift) / unit_q, rounded up: divides below 2^31
+  // Work: units_per_head * (H / pack) units, each in `split` key ranges; with more than
   // one, partial results are merged by k_cross_combine.
   int units_per_head, units, split;
   float* part_o;
@@ -107,19 +108,27 @@ struct CrossParams {
 
 __device__ __forceinline__ int clamped(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// First row of sequence b's queries (b = B: one past the last row).
+// First query of sequence b (b = B: one past the last).
 __device__ __forceinline__ int first_row(const CrossParams& p, int b) {
-  return (p.q_start != nullptr ? clamped(__ldg(p.q_start + b), 0, p.n) : b * (p.n / p.B)) << p.pack;
+  return p.q_start != nullptr ? clamped(__ldg(p.q_start + b), 0, p.n) : b * (p.n / p.B);
 }
 
-// Where row r of head group h starts in o.
+__device__ __forceinline__ int over_unit(const CrossParams& p, int q) {
+  return static_cast<int>(__umulhi(static_cast<uint32_t>(q), p.over_unit) >> p.unit_shift);
+}
+
+__device__ __forceinline__ int over_pack(const CrossParams& p, int r) {
+  return static_cast<int>(static_cast<uint32_t>(r) * p.over_pack >> 16);
+}
+
+// Where row r of a unit starts in o; the unit's first query is q0, its head group h.
 template <int HD>
-__device__ __forceinline__ __nv_bfloat16* out_row(const CrossParams& p, int h, int r) {
-  const int head = (h << p.pack) + (r & ((1 << p.pack) - 1));
-  return p.o + static_cast<size_t>(r >> p.pack) * p.ld + head * HD;
+__device__ __forceinline__ __nv_bfloat16* out_row(const CrossParams& p, int h, int q0, int r) {
+  const int q = over_pack(p, r);
+  return p.o + static_cast<size_t>(q0 + q) * p.ld + (h * p.pack + r - q * p.pack) * HD;
 }
 
-// Sequence and rows [q0, q1) of unit u of a head, by a 32-way search over the
+// Sequence and queries [q0, q1) of unit u of a head, by a 32-way search over the
 // sequences' first units; q0 >= q1: no rows.  Executed by whole warps.  The last
 // step's lanes hold the rows (and with `len`, the key counts) of all sequences
 // in question, so nothing is loaded again once the sequence is known.
@@ -134,7 +143,7 @@ __device__ __forceinline__ void unit_rows(const CrossParams& p, int u, int& b, i
     bool at_or_before = false;
     if (i < len || (step == 1 && i == len)) {  // the one past the last ends it
       row = first_row(p, lo + i);
-      at_or_before = i < len && row / kUnitQ + lo + i <= u;
+      at_or_before = i < len && over_unit(p, row) + lo + i <= u;
     }
     if (keys != nullptr && p.kv_len != nullptr && step == 1 && i < len)
       kv = clamped(__ldg(p.kv_len + lo + i), 0, p.S);
@@ -148,8 +157,8 @@ __device__ __forceinline__ void unit_rows(const CrossParams& p, int u, int& b, i
       const int first = __shfl_sync(0xffffffffu, row, c - 1);
       const int last = c < 32 ? __shfl_sync(0xffffffffu, row, c & 31) : first_row(p, b + 1);
       if (keys != nullptr) *keys = __shfl_sync(0xffffffffu, kv, c - 1);
-      q0 = first + (u - (first / kUnitQ + b)) * kUnitQ;
-      q1 = min(last, q0 + kUnitQ);
+      q0 = first + (u - (over_unit(p, first) + b)) * p.unit_q;
+      q1 = min(last, q0 + p.unit_q);
       return;
     }
     const int next = lo + (c - 1) * step;
@@ -233,6 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  if (warp > 1 && p.tile < kQ) {  // rows of Q that no copy reaches
+    const int per = (kQ - p.tile) * 8;
+    for (int i = threadIdx.x - 64; i < 2 * Cfg::kRegions * per; i += 32 * kSoftmaxWarps)
+      *reinterpret_cast<uint4*>(sQ + i / per * Cfg::kRegionBytes + p.tile * 128 + 16 * (i % per)) =
+          make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
   // The producer does not wait for the others' start: it set the barriers up
   // itself and uses no TMEM, so its search and first copies run under the
   // allocation.
@@ -264,8 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int unit = item / p.split, piece = item - unit * p.split;
         d.h = unit / p.units_per_head;
         int keys = 0;
-        unit_rows(p, unit - d.h * p.units_per_head, d.b, d.q0, d.q1, &keys);
-        rows = d.q0 < d.q1;
+        int q1;
+        unit_rows(p, unit - d.h * p.units_per_head, d.b, d.q0, q1, &keys);
+        rows = d.q0 < q1;
+        d.rows = (q1 - d.q0) * p.pack;
         if (rows) {
           if (d.b != seen_b) {
             seen_b = d.b;
@@ -287,9 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           desc[slot] = d;
           mbar_arrive(&d_full[slot]);  // releases the descriptor
         }
-        const int ntile = d.q0 + kQ < d.q1 ? 2 : 1;
+        const int ntile = d.rows > p.tile ? 2 : 1;
         const int bk = p.k_shared ? 0 : d.b, bv = p.v_shared ? 0 : d.b;
-        const int head = d.h << p.pack, kcol = head / p.group * HD;
+        const int head = d.h * p.pack, kcol = head / p.group * HD;
         for (int j = 0; j < d.nkv && ok; ++j, ++it) {
           const int s = it % kStages;
           const uint32_t ph = ((it / kStages) & 1) ^ 1;
@@ -309,11 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             ++nq;
-            mbar_arrive_expect_tx(q_full, ntile * Cfg::kTileBytes);
+            mbar_arrive_expect_tx(q_full, ntile * Cfg::kRegions * p.tile * 128);
             for (int t = 0; t < ntile; ++t)
               for (int r = 0; r < Cfg::kRegions; ++r)
                 tma_load_3d(sQ + t * Cfg::kTileBytes + r * Cfg::kRegionBytes, &tmQ, q_full, 64 * r, head,
-                            (d.q0 + t * kQ) >> p.pack);
+                            d.q0 + t * p.tile_q);
           }
           if (!mbar_wait(&v_empty[s], ph)) {
             (void)mbar_wait(&k_full[s], (it / kStages) & 1);
@@ -371,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const int nkv = desc[nd & 1].nkv;
-        const int ntile = desc[nd & 1].q0 + kQ < desc[nd & 1].q1 ? 2 : 1;
+        const int ntile = desc[nd & 1].rows > p.tile ? 2 : 1;
         mbar_arrive(&d_empty[nd & 1]);
         if (nkv < 0) break;
         if (nkv == 0) continue;
@@ -444,26 +462,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&d_empty[nd & 1]);
       if (d.nkv < 0) break;
-      const int warp_row = d.q0 + t * kQ + 32 * qd;  // first row of this warp
+      const int warp_row = t * p.tile + 32 * qd;              // this warp's first row of the unit
+      const int warp_end = min(d.rows, (t + 1) * p.tile);     // its last one is before this
       if (d.nkv == 0) {  // no key in this range: zeros, or an empty part
-        const int rows = min(32, d.q1 - warp_row);
+        const int rows = min(32, warp_end - warp_row);
         if (d.part >= 0) {
           if (lane < rows)
-            p.part_ml[static_cast<size_t>(d.part) * kUnitQ + t * kQ + row] = make_float2(-FLT_MAX, 0.f);
+            p.part_ml[static_cast<size_t>(d.part) * 2 * kQ + t * kQ + row] = make_float2(-FLT_MAX, 0.f);
         } else {
           for (int r = 0; r < rows; ++r)
             if (lane < HD / 8)
-              *reinterpret_cast<uint4*>(out_row<HD>(p, d.h, warp_row + r) + 8 * lane) =
+              *reinterpret_cast<uint4*>(out_row<HD>(p, d.h, d.q0, warp_row + r) + 8 * lane) =
                   make_uint4(0u, 0u, 0u, 0u);
         }
         continue;
       }
-      const int ntile = d.q0 + kQ < d.q1 ? 2 : 1;
+      const int ntile = d.rows > p.tile ? 2 : 1;
       if (t >= ntile) {
         it += d.nkv;
         continue;
       }
-      const bool mine = warp_row < d.q1;  // whether any of this warp's rows exists
+      const bool mine = warp_row < warp_end;  // whether any of this warp's rows exists
       const uint8_t* mrow = kMask ? p.kv_mask + static_cast<int64_t>(d.b) * p.S : nullptr;
       // the mask bytes of a tile's keys, four a lane, loaded one tile ahead
       uint32_t bytes[4] = {0u, 0u, 0u, 0u};
@@ -581,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mine) continue;
       tc_fence_after();
       if (d.part >= 0) {
-        const size_t prow = static_cast<size_t>(d.part) * kUnitQ + t * kQ + row;
-        const bool real = warp_row + lane < d.q1;
+        const size_t prow = static_cast<size_t>(d.part) * 2 * kQ + t * kQ + row;
+        const bool real = warp_row + lane < warp_end;
         if (real) p.part_ml[prow] = make_float2(m_run, l_run);
 #pragma unroll 1
         for (int c = 0; c < HD / 32; ++c) {
@@ -618,13 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pack_bf16(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv),
                 pack_bf16(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv));
           if (!(c & 1)) continue;
-          if (warp_row + 32 <= d.q1) {
-            // 32 rows of this sequence: one tiled store, which this warp does not
+          if (warp_row + 32 <= warp_end && p.tile == kQ) {
+            // 32 rows of this sequence, whole queries: one tiled store, which this warp does not
             // wait for (an SM stores about 32 bytes a clock: 2000 clocks a unit)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(&tmO, stage, 32 * (c - 1), d.h << p.pack, warp_row >> p.pack);
+              tma_store_3d(&tmO, stage, 32 * (c - 1), d.h * p.pack, d.q0 + over_pack(p, warp_row));
               tma_store_commit();
             }
           } else {
@@ -634,8 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int rr = 4 * k + (lane >> 3);
-              if (warp_row + rr < d.q1)
-                *reinterpret_cast<uint4*>(out_row<HD>(p, d.h, warp_row + rr) + 32 * (c - 1) + 8 * g) =
+              if (warp_row + rr < warp_end)
+                *reinterpret_cast<uint4*>(out_row<HD>(p, d.h, d.q0, warp_row + rr) + 32 * (c - 1) + 8 * g) =
                     *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (g ^ (rr & 7)));
             }
             __syncwarp();
@@ -665,17 +684,18 @@ __global__ void __launch_bounds__(256) k_cross_combine(const __grid_constant__ C
   const int h = unit / p.units_per_head;
   int b, q0, q1;
   unit_rows(p, unit - h * p.units_per_head, b, q0, q1);
-  if (rr >= q1 - q0) return;
+  const int row = rr / kQ * p.tile + rr % kQ;  // of the unit
+  if (rr % kQ >= p.tile || row >= (q1 - q0) * p.pack) return;
   const size_t part0 = static_cast<size_t>(blockIdx.y) * p.split;
   float M = -FLT_MAX;
-  for (int i = 0; i < p.split; ++i) M = fmaxf(M, p.part_ml[(part0 + i) * kUnitQ + rr].x);
+  for (int i = 0; i < p.split; ++i) M = fmaxf(M, p.part_ml[(part0 + i) * 2 * kQ + rr].x);
   constexpr int kPer = HD / 32;
   float acc[kPer];
 #pragma unroll
   for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
   float L = 0.f;
   for (int i = 0; i < p.split; ++i) {
-    const size_t prow = (part0 + i) * kUnitQ + rr;
+    const size_t prow = (part0 + i) * 2 * kQ + rr;
     const float2 ml = p.part_ml[prow];
     if (ml.y == 0.f) continue;
     const float wgt = ex2_approx(ml.x - M);
@@ -685,7 +705,7 @@ __global__ void __launch_bounds__(256) k_cross_combine(const __grid_constant__ C
     for (int c = 0; c < kPer; ++c) acc[c] += po[lane + 32 * c] * wgt;
   }
   const float inv = L == 0.f ? 0.f : 1.0f / L;
-  __nv_bfloat16* orow = out_row<HD>(p, h, q0 + rr);
+  __nv_bfloat16* orow = out_row<HD>(p, h, q0, row);
 #pragma unroll
   for (int c = 0; c < kPer; ++c) orow[lane + 32 * c] = __float2bfloat16_rn(acc[c] * inv);
 }
@@ -703,17 +723,17 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
   // Packed heads and key ranges per unit: the rounds of CTAs times the tiles of a
   // range, plus two tiles' time for a unit's own ends and six for the merge,
   // whichever is least.  Packing the query heads of a key head fills the tiles
-  // of short sequences; where it saves no round, heads of their own load less
-  // at once (100 queries, 24 heads of 4 key heads x 128, 512 keys: 12.7 us
-  // against 14.5 with two heads a tile; 8 sequences of two queries, 32 heads of 2,
-  // 4096 keys: 17.4 us against 105.6 without).
+  // of short sequences (16 sequences of one query, 40 heads of 8 x 128, 1000 keys: 59 us
+  // with heads of their own, 18.7 with five a tile); where it saves no round, heads
+  // of their own load less at once (100 queries, 24 heads of 4 x 128, 512 keys:
+  // 12.7 us, 14.5 with two a tile).
   const int tiles = (a.S + kKV - 1) / kKV;
   constexpr int kMaxUnits = 0x3fffffff / kMaxSplitParts;
   int64_t best = INT64_MAX;
-  for (int pack = 0; (1 << pack) <= kMaxPack && p.group % (1 << pack) == 0; ++pack) {
-    const int64_t rows = static_cast<int64_t>(a.n) << pack;
-    const int64_t units64 = (rows / kUnitQ + a.B) * (H >> pack);
-    if (rows > INT_MAX || units64 > kMaxUnits) continue;
+  for (int pack = 1; pack <= kMaxPack; ++pack) {
+    if (p.group % pack != 0) continue;
+    const int64_t units64 = (static_cast<int64_t>(a.n / (2 * (kQ / pack))) + a.B) * (H / pack);
+    if (units64 > kMaxUnits) continue;
     const int units = static_cast<int>(units64);
     for (int sp = 1; sp <= tiles && sp <= kMaxSplitParts && (sp == 1 || units * sp <= kMaxAttnParts); ++sp) {
       const int rounds = (units * sp + c.num_sms - 1) / c.num_sms;
@@ -721,7 +741,7 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
       if (cost >= best) continue;
       best = cost;
       p.units = units;
-      p.units_per_head = units / (H >> pack);
+      p.units_per_head = units / (H / pack);
       p.pack = pack;
       p.split = sp;
     }
@@ -730,14 +750,21 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
     if (why) *why = "too many sequences";
     return cudaErrorInvalidValue;
   }
-  const uint32_t heads = 1u << p.pack;  // Q and O as [queries][heads][columns]
+  p.tile_q = kQ / p.pack;
+  p.tile = p.tile_q * p.pack;
+  p.unit_q = 2 * p.tile_q;
+  p.over_pack = static_cast<uint32_t>((65536 + p.pack - 1) / p.pack);
+  while ((2 << p.unit_shift) < p.unit_q) ++p.unit_shift;
+  const uint64_t scaled = 1ull << (32 + p.unit_shift);
+  p.over_unit = static_cast<uint32_t>((scaled + p.unit_q - 1) / p.unit_q);
+  const uint32_t heads = p.pack;  // Q and O as [queries][heads][columns]
   CUtensorMap tq, tk, tv, to;
-  if (!make_tmap_bf16_3d(&tq, a.q, a.n, H, HD, HD, D, heads, why, kQ / heads)) return cudaErrorInvalidValue;
+  if (!make_tmap_bf16_3d(&tq, a.q, a.n, H, HD, HD, D, heads, why, p.tile_q)) return cudaErrorInvalidValue;
   if (!make_tmap_bf16_3d(&tk, a.k, k1 ? 1 : a.B, a.S, width, a.ld_k, k1 ? a.ld_k * a.S : a.bs_k, kKV, why))
     return cudaErrorInvalidValue;
   if (!make_tmap_bf16_3d(&tv, a.v, v1 ? 1 : a.B, a.S, width, a.ld_v, v1 ? a.ld_v * a.S : a.bs_v, kKV, why))
     return cudaErrorInvalidValue;
-  if (!make_tmap_bf16_3d(&to, a.o, a.n, H, HD, HD, D, heads, why, 32 / heads)) return cudaErrorInvalidValue;
+  if (!make_tmap_bf16_3d(&to, a.o, a.n, H, HD, HD, D, heads, why, 32 % heads == 0 ? 32 / heads : 1)) return cudaErrorInvalidValue;
   p.k_shared = k1;
   p.v_shared = v1;
   const double scale = a.scale != 0.f ? a.scale : 1.0 / sqrt(static_cast<double>(HD));
@@ -765,7 +792,7 @@ cudaError_t launch_hd(const Ctx& c, const hsa_cross_args& a, std::string* why) {
   c.launches += 1;
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.split == 1) return e;
-  k_cross_combine<HD><<<dim3(kUnitQ / 8, p.units), 256, 0, c.stream>>>(p);
+  k_cross_combine<HD><<<dim3(2 * kQ / 8, p.units), 256, 0, c.stream>>>(p);
   c.launches += 1;
   return cudaGetLastError();
 }
