@@ -11,7 +11,7 @@
 // merged over the groups of a warp by shuffles, over the warps of a CTA in shared
 // memory and over the CTAs of a cluster, which split the keys when there are
 // few sequences, through distributed shared memory.  16 sequences of one query,
-// 12 heads x 128, up to 512 keys: 11.5 us (24 in 128-query tiles; the bytes alone take 5.5).
+// 12 heads x 128, up to 512 keys: 11.5 us (the bytes alone take 5.5).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
