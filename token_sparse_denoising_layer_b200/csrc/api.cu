@@ -158,6 +158,7 @@ namespace {
 template <typename Layer>
 hsa_status step(hsa_ctx* ctx, const hsa_model_weights* w, const hsa_state* s, int i, float sigma_i,
                 float sigma_next, int regroup, Layer layer) {
+  hsa::DeviceScope dev(ctx->c.device);
   int n = 0;
   hsa_status st = hsa_schedule(ctx, i, s->g, s->mask, s->active_idx, nullptr, &n);
   if (st == HSA_OK) st = hsa_embed(ctx, w->w_in, s->x, s->active_idx, n, s->h);
@@ -1018,6 +1019,7 @@ hsa_status quant_mlp(hsa_ctx* ctx, const hsa_layer_weights_quant& w, float* x, c
 hsa_status hsa_layer_forward_ext(hsa_ctx* ctx, const hsa_layer_weights* w, const hsa_block_ext* ext,
                                  float* x, const int32_t* idx, int n, void* k_cache, void* v_cache) {
   HSA_CHECK_CTX(ctx);
+  hsa::DeviceScope dev(ctx->c.device);
   const hsa_block_ext b = ext != nullptr ? *ext : hsa_block_ext{};
   const float* mod = b.mod;
   const hsa_cross_attn* xa = b.xa;
