@@ -88,3 +88,11 @@ def test_launches_go_to_the_contexts_device(lib, ctx, call, launches):
     assert lib.fake_launches() - before == launches
     assert lib.fake_strays() == strays
     assert lib.fake_device() == 0  # and the caller's device is current again
+
+
+def test_a_kernels_attribute_is_set_on_the_device_it_is_noted_for(lib):
+    lib.fake_set_device(0)
+    assert lib.fake_ensure_smem_limit(1) == 1
+    assert lib.fake_ensure_smem_limit(1) == -1  # once per device
+    assert lib.fake_ensure_smem_limit(0) == 0
+    assert lib.fake_device() == 0

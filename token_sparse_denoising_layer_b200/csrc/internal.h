@@ -118,17 +118,6 @@ __device__ __forceinline__ bool row_ok(int32_t r, int N, int* flag) {
   return false;
 }
 
-// Raise a kernel's dynamic shared-memory limit, once per device (bit d of `done`).
-template <typename Kernel>
-cudaError_t ensure_smem_limit(Kernel* kernel, int bytes, int device, std::atomic<uint64_t>& done) {
-  const uint64_t bit = 1ull << (device & 63);
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
-  return e;
-}
-
 // Makes the context's device current for a scope, so that a call works from a
 // thread whose current device is another one.
 class DeviceScope {
@@ -147,6 +136,19 @@ class DeviceScope {
  private:
   int old_ = -1;
 };
+
+// Raise a kernel's dynamic shared-memory limit on a device, once (bit d of `done`).
+// The runtime sets the attribute for the current device, so that one is made current.
+template <typename Kernel>
+cudaError_t ensure_smem_limit(Kernel* kernel, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = 1ull << (device & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  DeviceScope scope(device);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
 
 // ---- launchers (return cudaGetLastError() of the launch)
 cudaError_t launch_schedule(const Ctx& c, int i, const uint8_t* g, uint8_t* mask, int32_t* idx,
