@@ -579,8 +579,10 @@ typedef struct {
  *   v_cache (device) bf16 [N, D] and v_in, rows ld_v apart: both or neither.
  *   ld_* multiples of 8, >= D; 0 <= n <= N; D <= 10240 (HSA_ERR_SHAPE beyond).
  * q may be q_in; no other output may overlap an input.  A row with an index or table row out of range
- * (or, in place, an index not above the one before it) is skipped, its q row
- * zeroed if that was to be written, and reported by hsa_sync_check.
+ * (or, with keys in place, an index not above the one before it) is skipped whole: its cache rows
+ * keep their key and value, its q row is zeroed if that was to be written, and
+ * hsa_sync_check reports it.  (Order is judged by neighbours alone: in place, a reported
+ * list that names a row twice may have turned that row twice.)
  */
 hsa_status hsa_qk_norm_rope(hsa_ctx* ctx, const hsa_qk_rope* a, const int32_t* idx,
                             const int32_t* pos, int n, const void* q_in, int64_t ld_q, void* q,

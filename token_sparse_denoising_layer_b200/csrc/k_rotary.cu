@@ -333,6 +333,7 @@ struct QkParams {
   const int32_t *idx, *pos;
   int n, N, P, H, rot, norm, parts;
   uint8_t part[3];  // what each of the `parts` warps of a row does: 0 q, 1 k, 2 v
+  bool ascending;   // keys in place: a row named twice would be turned twice, so idx must ascend
   float eps;
   int* flag;
 };
@@ -403,16 +404,17 @@ __global__ void __launch_bounds__(32 * kQkWarps, NIT <= 3 ? 6 : 1)
     }
   };
   if (!in_place) load_row();
+  // One verdict for the row's parts, so that no value is written beside a key
+  // that was skipped.
   bool good = row_ok(r, p.N, p.flag);
-  if (rotating) good = row_ok(trow, p.P, p.flag) && good;
-  __nv_bfloat16* dst = part == 0 ? p.q + static_cast<int64_t>(m) * D
-                                 : (part == 1 ? p.k_cache : p.v_cache) + static_cast<int64_t>(r) * D;
-  const float* w = part == 0 ? p.w_q : p.w_k;
-  if (in_place && m > 0 && p.idx != nullptr && __ldg(p.idx + m - 1) >= r) {
-    // a row named twice would be turned twice: the list must ascend
+  if (p.table != nullptr) good = row_ok(trow, p.P, p.flag) && good;
+  if (p.ascending && m > 0 && __ldg(p.idx + m - 1) >= r) {
     if (lane == 0) atomicOr(p.flag, DEV_BAD_INDEX);
     good = false;
   }
+  __nv_bfloat16* dst = part == 0 ? p.q + static_cast<int64_t>(m) * D
+                                 : (part == 1 ? p.k_cache : p.v_cache) + static_cast<int64_t>(r) * D;
+  const float* w = part == 0 ? p.w_q : p.w_k;
   if (!good) {  // skipped and reported; a query row is left zero rather than unset
     if (part == 0)
       for (int e = 8 * lane; e < D; e += 256)
@@ -578,6 +580,7 @@ cudaError_t launch_qk_norm_rope(const Ctx& c, const hsa_qk_rope& a, const QkRows
   p.w_k = a.w_k;
   p.table = a.table;
   p.idx = r.idx;
+  p.ascending = r.k_cache != nullptr && r.k_in == nullptr && r.idx != nullptr;
   p.pos = r.pos;
   p.n = r.n;
   p.N = c.cfg.N;
