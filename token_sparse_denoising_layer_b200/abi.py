@@ -608,15 +608,18 @@ def hsa_cross_attention(ctx: Context, q, q_start, n: int, B: int, k, v, S: int, 
                         kv_mask=None, kv_heads: Optional[int] = None, scale: float = 0.0) -> None:
     """q, o bf16 [n, D]; q_start int32 [B + 1] or None (n / B rows each); k, v bf16 [B, S, kv_heads * D/H] (rows and
     sequences may be strided, a sequence distance of 0 shares one); kv_len int32 [B];
-    kv_mask uint8 or bool [B, S], non-zero = seen (include/hsa.h)."""
+    kv_mask uint8 or bool [B, S] (or flat), non-zero = seen (include/hsa.h)."""
     D, H = ctx.cfg.D, ctx.cfg.H
     kvh = H if kv_heads is None else kv_heads
     width = kvh * (D // H)
     pk, ldk, bsk = _padded(ctx, k, B, S, width, "k")
     pv, ldv, bsv = _padded(ctx, v, B, S, width, "v")
-    if kv_mask is not None and _dtype(kv_mask) == "bool":
-        import torch
-        kv_mask = kv_mask.view(torch.uint8)
+    if kv_mask is not None:
+        if B > 1 and kv_mask.dim() > 1 and kv_mask.shape[-1] != S:  # its rows are read S bytes apart
+            raise ValueError(f"kv_mask needs rows of S = {S}, has {tuple(kv_mask.shape)}")
+        if _dtype(kv_mask) == "bool":
+            import torch
+            kv_mask = kv_mask.view(torch.uint8)
     args = hsa_cross_args(_typed(ctx, q, n * D, "bfloat16", "q"),
                           _typed(ctx, q_start, B + 1, "int32", "q_start"), n, B, pk, pv, ldk, bsk, ldv,
                           bsv, S, kvh, _typed(ctx, kv_len, B, "int32", "kv_len"),
