@@ -450,21 +450,36 @@ def _on_device(ctx: "Optional[Context]", t, what: str) -> None:
         raise ValueError(f"{what} is on cuda:{where}, the context on cuda:{ctx.device}")
 
 
-def _typed(ctx: Optional[Context], t, n: int, dtype: str, what: str) -> Optional[int]:
-    """Device address of a contiguous tensor of at least n elements of a type."""
+def _typed(ctx: Optional[Context], t, n: int, dtype: str, what: str, row: int = 0) -> Optional[int]:
+    """Device address of a contiguous tensor of at least n elements of a type; with
+    `row`, of one that is read as dense rows of that many."""
     if t is None:
         return None
+    have = t.numel()
     if (ctx is not None and t.dtype is _dtype_names.get(dtype) and t.get_device() == ctx.device
-            and t.numel() >= n and t.is_contiguous()):
+            and (have == n or have > n and row == 0) and t.is_contiguous()):
         return t.data_ptr()  # (most calls: a call's checks are a good part of its host time)
     if _dtype(t) != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.numel() < n:
-        raise ValueError(f"{what} needs {n} elements, has {t.numel()}")
+    if have < n:
+        raise ValueError(f"{what} needs {n} elements, has {have}")
     _on_device(ctx, t, what)
     if not t.is_contiguous():
         raise ValueError("libhsa takes contiguous tensors")
+    if row and have > n > row and t.dim() > 1:  # longer rows (a flat tensor's have any length)
+        length = 1
+        for x in reversed(t.shape):  # trailing axes that make up a row
+            length *= x
+            if length >= row:
+                break
+        if length != row:
+            raise ValueError(f"{what} needs rows of {row}, has {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _planes(table, rot: int) -> int:
+    """Row length that a rotary table [P, rot/2, 2] has to have (one of fewer axes may have any)."""
+    return rot if table is not None and table.dim() == 3 else 0
 
 
 def _rows(ctx: Context, t, n: int, width: int, dtypes: Sequence[str], what: str):
@@ -530,7 +545,7 @@ def hsa_rope_table(ctx: Context, cfg: hsa_rope_cfg, pos, P: int, table) -> None:
     """pos int32 [P, n_axes] or None (one axis, positions 0..P-1); table fp32 [P, rot/2, 2]."""
     rot = sum(cfg.dims[:max(0, min(cfg.n_axes, 3))])
     _check(ctx.ptr, load().hsa_rope_table(ctx.ptr, ctypes.byref(cfg),
-                                          _typed(ctx, pos, P * cfg.n_axes, "int32", "pos"), P,
+                                          _typed(ctx, pos, P * cfg.n_axes, "int32", "pos", cfg.n_axes), P,
                                           _typed(ctx, table, P * rot, "float32", "table")))
 
 
@@ -542,7 +557,7 @@ def hsa_rope(ctx: Context, x, n: int, heads: int, table, P: int, rot: int, out,
     po, ldo = _rows(ctx, out, n, width, (_dtype(x),), "out")
     kind = 1 if _dtype(x) == "float32" else 0
     _check(ctx.ptr, load().hsa_rope(ctx.ptr, px, ldx, kind, n, heads,
-                                    _typed(ctx, table, P * rot, "float32", "table"), P, rot,
+                                    _typed(ctx, table, P * rot, "float32", "table", _planes(table, rot)), P, rot,
                                     _typed(ctx, pos, n, "int32", "pos"), _choice(ROPE_LAYOUT, layout, "layout"),
                                     1 if inverse else 0, po, ldo))
 
@@ -552,7 +567,7 @@ def qk_rope(norm: str = "head", w_q=None, w_k=None, eps: float = 1e-6, table=Non
     """The struct holds raw device addresses, so it also keeps the tensors alive."""
     s = hsa_qk_rope(_choice(QK_NORM, norm, "norm"), _typed(None, w_q, 1, "float32", "w_q"),
                     _typed(None, w_k, 1, "float32", "w_k"), eps,
-                    _typed(None, table, P * rot, "float32", "table"), P, rot,
+                    _typed(None, table, P * rot, "float32", "table", _planes(table, rot)), P, rot,
                     _choice(ROPE_LAYOUT, layout, "layout"))
     s._keep = [t for t in (w_q, w_k, table) if t is not None]
     s._widths = [t.numel() for t in (w_q, w_k) if t is not None]
@@ -585,9 +600,9 @@ def hsa_qk_norm_rope(ctx: Context, a: hsa_qk_rope, idx, n: int, q, k_cache=None,
     pv, ldv = _rows(ctx, v_in, n, D, ("bfloat16",), "v_in")
     _check(ctx.ptr, load().hsa_qk_norm_rope(
         ctx.ptr, ctypes.byref(a), _typed(ctx, idx, n, "int32", "idx"), _typed(ctx, pos, n, "int32", "pos"),
-        n, pq, ldq, _typed(ctx, q, n * D, "bfloat16", "q"), pk, ldk,
-        _typed(ctx, k_cache, N * D, "bfloat16", "k_cache"), pv, ldv,
-        _typed(ctx, v_cache, N * D, "bfloat16", "v_cache")))
+        n, pq, ldq, _typed(ctx, q, n * D, "bfloat16", "q", D), pk, ldk,
+        _typed(ctx, k_cache, N * D, "bfloat16", "k_cache", D), pv, ldv,
+        _typed(ctx, v_cache, N * D, "bfloat16", "v_cache", D)))
 
 
 def _padded(ctx: Context, t, B: int, S: int, width: int, what: str):
@@ -620,7 +635,7 @@ def hsa_cross_attention(ctx: Context, q, q_start, n: int, B: int, k, v, S: int, 
         if _dtype(kv_mask) == "bool":
             import torch
             kv_mask = kv_mask.view(torch.uint8)
-    args = hsa_cross_args(_typed(ctx, q, n * D, "bfloat16", "q"),
+    args = hsa_cross_args(_typed(ctx, q, n * D, "bfloat16", "q", D),
                           _typed(ctx, q_start, B + 1, "int32", "q_start"), n, B, pk, pv, ldk, bsk, ldv,
                           bsv, S, kvh, _typed(ctx, kv_len, B, "int32", "kv_len"),
                           _typed(ctx, kv_mask, B * S, "uint8", "kv_mask"), scale,
