@@ -9,7 +9,7 @@ sections 2.1-2.3.
 
 from __future__ import annotations
 
-from typing import Optional, Sequence
+from typing import Optional, Sequence, Union
 
 import numpy as np
 
@@ -90,21 +90,34 @@ class HsaLoop:
             abi.hsa_step_cond(self.ctx, self.model, cond, i, float(self.sigmas[i]),
                               float(self.sigmas[i + 1]), regroup)
 
+    def _exts(self, ext, steps: int) -> list:
+        """The extension of each iteration from `ext`: one for all, or a sequence with one each."""
+        if ext is None or isinstance(ext, abi.StepExt):
+            return [ext] * steps
+        exts = list(ext)
+        if len(exts) < steps:
+            raise ValueError(f"{len(exts)} extensions for {steps} iterations")
+        return exts[:steps]
+
     def run(self, regroup: bool = True, stop: Optional[int] = None,
-            ext: "Optional[abi.StepExt]" = None):
-        for i in range(self.T if stop is None else stop):
-            self.step(i, regroup, ext=ext)
+            ext: "Union[abi.StepExt, Sequence[Optional[abi.StepExt]], None]" = None):
+        """Iterations 0..stop-1 (all T of them).  ``ext`` is one abi.StepExt for all of
+        them, or one per iteration: a timestep's modulation differs from one to the next."""
+        exts = self._exts(ext, self.T if stop is None else stop)
+        for i, e in enumerate(exts):
+            self.step(i, regroup, ext=e)
         return self.x
 
-    def capture(self, regroup: bool = True, ext: "Optional[abi.StepExt]" = None) -> None:
-        """Record the whole loop, i = 0..T-1, as one CUDA graph.
+    def capture(self, regroup: bool = True,
+                ext: "Union[abi.StepExt, Sequence[Optional[abi.StepExt]], None]" = None) -> None:
+        """Record the whole loop, i = 0..T-1, as one CUDA graph; ``ext`` as in run().
 
         Every step's launch shape is fixed by the host (|A_i| follows from the
         group counts), so the T steps replay as recorded; the graph reads and
         writes this loop's buffers in place.  Call after at least one eager
         step (first calls set kernel attributes), and reset() before replay()."""
         t = self.torch
-        self._captured_ext = ext  # the graph holds its addresses
+        exts = self._exts(ext, self.T)
         t.cuda.synchronize()
         side = t.cuda.Stream()
         g = t.cuda.CUDAGraph()
@@ -112,12 +125,13 @@ class HsaLoop:
         abi.hsa_set_stream(self.ctx, side)
         try:
             with t.cuda.graph(g, stream=side):
-                for i in range(self.T):
-                    self.step(i, regroup, ext=ext)
+                for i, e in enumerate(exts):
+                    self.step(i, regroup, ext=e)
         finally:
             abi.hsa_set_stream(self.ctx, self._stream)
         self.graph_launches = abi.hsa_kernel_launches(self.ctx) - n0
         self.graph = g
+        self._captured_ext = exts  # the graph holds their addresses
 
     def replay(self) -> None:
         """Run the recorded loop on the current stream."""
