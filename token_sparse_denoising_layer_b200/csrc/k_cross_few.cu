@@ -54,6 +54,7 @@ struct FewParams {
   int ld;  // D
   int n, B, S, kv_heads, group, split;
   float scale_log2;
+  float even;  // passes of sequences of equal length, as further_rows numbers them: sequences a pass
   const int32_t *q_start, *kv_len;
   const uint8_t* kv_mask;
   int* flag;
@@ -84,6 +85,60 @@ struct Run {
   }
 };
 
+// A sequence of more than R rows (queries x the heads of a key head) takes more passes over
+// its keys than the one by the CTA of its number.  These are numbered so that
+// sequence b's second one is floor(its first row / R): with floor(x + y) >= floor(x) +
+// floor(y) every sequence has room for its own, and their number is at most
+// floor(n group / R) <= B (launch_cross_few chooses R so).  So each CTA has one
+// at most beside its first, however unequal the sequences are: pass `slot`, here found
+// in q_start as sequence b and first row r0 (b = -1: no such pass).  (32 sequences of
+// 12 heads x 128, 512 keys, 31 with one query and one with 97: 59 us; 362 with all of a
+// sequence's passes in one CTA.)
+//
+// Where sequences fill their pass, sequence `slot` (rows [q0, q1)) has the pass's number
+// itself.  Else the search begins with the 32 sequences around the place that even
+// lengths would give it, whose offsets arrive with the CTA's own.  (16 sequences of one
+// query: 10.8 us with and without, 4 rows a key head 27.2 and 26.7; a search of all of q_start after the
+// first pass 11.8 and 28.0.)
+template <int R>
+__device__ __forceinline__ void further_rows(const FewParams& p, int slot, int q0, int q1, int& b, int& r0) {
+  const int lane = threadIdx.x & 31;
+  b = -1, r0 = 0;
+  if (p.q_start == nullptr || slot >= p.n * p.group / R) return;  // (equal parts have R rows at most)
+  int step = 1, len = p.B;
+  int lo = max(0, min(static_cast<int>(slot * p.even), p.B - 16) - 15);
+  int row = __ldg(p.q_start + min(lo + lane, p.B));
+  if (q0 * p.group / R <= slot && slot < q1 * p.group / R) {
+    r0 = (slot - q0 * p.group / R + 1) * R;
+    if (r0 < (q1 - q0) * p.group) b = slot;
+    return;
+  }
+  // lane i: whether the numbers of sequence lo + i step begin at or before slot
+  for (bool guessed = true;; guessed = false) {
+    const int i = lo + lane * step;
+    row = clamped(guessed ? row : __ldg(p.q_start + min(i, p.B)), 0, p.n);
+    const int at = row * p.group / R;
+    const uint32_t begun = __ballot_sync(0xffffffffu, i < (guessed ? p.B : lo + len) && at <= slot);
+    const int c = __popc(begun);
+    if (c > 0 && step == 1 && (c < 32 || !guessed)) {
+      const int first = __shfl_sync(0xffffffffu, at, c - 1), first_row = __shfl_sync(0xffffffffu, row, c - 1);
+      const int next = c < 32 ? __shfl_sync(0xffffffffu, row, c & 31) : clamped(__ldg(p.q_start + lo + 32), 0, p.n);
+      r0 = (slot - first + 1) * R;
+      if (first <= slot && r0 < (next - first_row) * p.group) b = lo + c - 1;
+      return;
+    }
+    if (guessed) {
+      if (c == 0 && lo == 0) return;  // rows before the first sequence
+      lo = 0;
+    } else {
+      if (c == 0) return;
+      lo += (c - 1) * step;
+      len = min(step, len - (c - 1) * step);
+    }
+    step = (len + 31) / 32;
+  }
+}
+
 template <int HD, int R>
 __global__ void __launch_bounds__(32 * warps_of<R>(), R == 1 ? 3 : 2)
     k_cross_few(const __grid_constant__ FewParams p) {
@@ -100,25 +155,36 @@ __global__ void __launch_bounds__(32 * warps_of<R>(), R == 1 ? 3 : 2)
 
   const int rank = blockIdx.x % p.split;
   const int item = blockIdx.x / p.split;
-  const int kvh = item % p.kv_heads, b = item / p.kv_heads;
+  const int kvh = item % p.kv_heads, slot = item / p.kv_heads;
   const int each = p.n / p.B;  // rows a sequence where q_start is not given
-  const int raw0 = p.q_start != nullptr ? __ldg(p.q_start + b) : b * each;
-  const int raw1 = p.q_start != nullptr ? __ldg(p.q_start + b + 1) : raw0 + each;
-  const int raw_len = p.kv_len != nullptr ? __ldg(p.kv_len + b) : p.S;
+  const int raw0 = p.q_start != nullptr ? __ldg(p.q_start + slot) : slot * each;
+  const int raw1 = p.q_start != nullptr ? __ldg(p.q_start + slot + 1) : raw0 + each;
+  int raw_len = p.kv_len != nullptr ? __ldg(p.kv_len + slot) : p.S;
+  int q0 = clamped(raw0, 0, p.n), q1 = clamped(raw1, 0, p.n);
   if (threadIdx.x == 0 && (raw0 < 0 || raw1 > p.n || raw0 > raw1 || raw_len < 0 || raw_len > p.S))
     atomicOr(p.flag, DEV_BAD_INDEX);
-  const int q0 = clamped(raw0, 0, p.n), q1 = clamped(raw1, 0, p.n);
-  if (q0 >= q1) return;  // the same for every CTA of the cluster
-  const int len = clamped(raw_len, 0, p.S);
-  const int rows = (q1 - q0) * p.group;
-  const __nv_bfloat16* kb = p.k + b * p.bs_k + kvh * HD + e;
-  const __nv_bfloat16* vb = p.v + b * p.bs_v + kvh * HD + e;
-  const uint8_t* mask = p.kv_mask == nullptr ? nullptr : p.kv_mask + static_cast<int64_t>(b) * p.S;
-  // this CTA's keys, a multiple of a warp's batch
-  const int per = ((len + p.split - 1) / p.split + G * kBatch - 1) / (G * kBatch) * (G * kBatch);
-  const int first = min(len, rank * per), last = min(len, first + per);
+  // First the first rows of sequence `slot`, then further rows of a longer one, if there
+  // are such: the same for every CTA of the cluster.
+  int further, further_r0;
+  further_rows<R>(p, slot, q0, q1, further, further_r0);
+  for (int turn = 0; turn < 2; ++turn) {
+    const int b = turn == 0 ? slot : further, r0 = turn == 0 ? 0 : further_r0;
+    if (b < 0) break;
+    if (turn > 0) {
+      q0 = clamped(__ldg(p.q_start + b), 0, p.n);
+      q1 = clamped(__ldg(p.q_start + b + 1), 0, p.n);
+      if (p.kv_len != nullptr) raw_len = __ldg(p.kv_len + b);
+    }
+    const int rows = (q1 - q0) * p.group;
+    if (r0 >= rows) continue;
+    const int len = clamped(raw_len, 0, p.S);
+    const __nv_bfloat16* kb = p.k + b * p.bs_k + kvh * HD + e;
+    const __nv_bfloat16* vb = p.v + b * p.bs_v + kvh * HD + e;
+    const uint8_t* mask = p.kv_mask == nullptr ? nullptr : p.kv_mask + static_cast<int64_t>(b) * p.S;
+    // this CTA's keys, a multiple of a warp's batch
+    const int per = ((len + p.split - 1) / p.split + G * kBatch - 1) / (G * kBatch) * (G * kBatch);
+    const int first = min(len, rank * per), last = min(len, first + per);
 
-  for (int r0 = 0; r0 < rows; r0 += R) {
     // A thread copies and reads its own places only, so the ring has no barriers.
     auto place = [&](int stage, int u, int kv) -> uint4& {
       return ring[((stage * kBatch + u) * 2 + kv) * (32 * kWarps) + threadIdx.x];
@@ -338,7 +404,8 @@ cudaError_t launch_rows(const Ctx& c, const FewParams& p) {
 cudaError_t launch_cross_few(const Ctx& c, const hsa_cross_args& a, bool* taken) {
   const int H = c.cfg.H, hd = c.cfg.D / H, group = H / a.kv_heads;
   const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads;
-  // One pass over the keys for a sequence of average length.  With more rows the
+  // One pass over the keys for a sequence of average length (see further_rows for
+  // longer ones).  With more rows the
   // 128-row tiles are as fast (16 sequences, 2 key heads, 2000 keys: 4 rows a key
   // head 14.3 us here, 8 rows 15.4 there).
   const int64_t rows = static_cast<int64_t>(a.n) * group;
@@ -371,6 +438,7 @@ cudaError_t launch_cross_few(const Ctx& c, const hsa_cross_args& a, bool* taken)
   p.split = 1;
   while (p.split < 8 && items * p.split < 2 * c.num_sms && a.S >= 2 * p.split * batch) p.split *= 2;
   const int r = rows <= a.B ? 1 : rows <= 2 * static_cast<int64_t>(a.B) ? 2 : kFewRows;
+  p.even = static_cast<float>(static_cast<double>(a.B) * r / static_cast<double>(rows));
   if (hd == 128)
     return r == 1 ? launch_rows<128, 1>(c, p) : r == 2 ? launch_rows<128, 2>(c, p) : launch_rows<128, kFewRows>(c, p);
   return r == 1 ? launch_rows<64, 1>(c, p) : r == 2 ? launch_rows<64, 2>(c, p) : launch_rows<64, kFewRows>(c, p);
