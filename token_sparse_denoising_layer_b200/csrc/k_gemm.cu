@@ -655,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       int it = 0, lt = 0;
       for (int t = pair; t < total_tiles && ok; t += npairs, ++lt) {
         const int b = lt & 1;
-        if (!mbar_wait(&acc_empty[b], ((lt >> 1) & 1) ^ 1)) {
+        if (!mbar_wait<true>(&acc_empty[b], ((lt >> 1) & 1) ^ 1)) {  // both CTAs' epilogues
           ok = false;
           break;
         }
