@@ -528,7 +528,8 @@ typedef struct {
 
 /*
  * Table of a rotary position embedding: table[p][i] = amp (cos, sin)(pos[p][axis(i)] f_i).
- * Angles are reduced to a turn in 64 bits, so far positions keep full fp32 accuracy.
+ * Angles are counted in 64-bit fractions of a turn: an entry is within 2^-21 amp of
+ * the exact one at every int32 position (an absolute bound: a small sine keeps fewer bits).
  *   cfg (host);  pos (device) int32 [P, n_axes], or NULL with one axis: row p has position p;
  *   table (device) fp32 [P, rot / 2, 2] out.   P >= 0.
  */

@@ -802,24 +802,27 @@ hsa_status hsa_rope_table(hsa_ctx* ctx, const hsa_rope_cfg* cfg, const int32_t* 
   if (P < 0) return fail(ctx, HSA_ERR_INVALID_ARG, "P must be >= 0");
   if (P == 0) return HSA_OK;
   HSA_CHECK_PTR(ctx, table);
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  // 64 bits of mantissa: a frequency's error grows with the position, and a
+  // double's (2^-56 turns) would pass fp32's at positions near 2^31.
+  constexpr long double kTwoPi = 6.283185307179586476925286766559005768L;
+  const long double factor = c.factor, fast = c.fast, slow = c.slow;
   hsa::RopeFreqs f{};
   f.half = rot / 2;
   f.n_axes = c.n_axes;
   f.amp = static_cast<float>(c.amp);
   for (int x = 0, j = 0; x < c.n_axes; ++x) {
-    const double dim = c.dims[x];
-    const double base = c.scaling == HSA_ROPE_BASE && dim > 2.0
-                            ? c.base * pow(c.factor, dim / (dim - 2.0)) : c.base;
+    const long double dim = c.dims[x];
+    const long double base = c.scaling == HSA_ROPE_BASE && dim > 2.0L
+                                 ? c.base * powl(factor, dim / (dim - 2.0L)) : c.base;
     for (int i = 0; i < c.dims[x] / 2; ++i, ++j) {
-      double w = pow(base, -2.0 * i / dim);
-      if (c.scaling == HSA_ROPE_LINEAR) w /= c.factor;
+      long double w = powl(base, -2.0L * i / dim);
+      if (c.scaling == HSA_ROPE_LINEAR) w /= factor;
       if (c.scaling == HSA_ROPE_PARTS) {
-        double keep = (c.orig_len * w / kTwoPi - c.slow) / (c.fast - c.slow);
-        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
-        w = (1.0 - keep) * w / c.factor + keep * w;
+        long double keep = (c.orig_len * w / kTwoPi - slow) / (fast - slow);
+        keep = keep < 0.0L ? 0.0L : keep > 1.0L ? 1.0L : keep;
+        w = (1.0L - keep) * w / factor + keep * w;
       }
-      f.turns[j] = static_cast<uint64_t>(ldexp(w / kTwoPi, 64));  // w <= 1
+      f.turns[j] = static_cast<uint64_t>(llrintl(ldexpl(w / kTwoPi, 64)));  // w <= 1
       f.axis[j] = static_cast<uint8_t>(x);
     }
   }

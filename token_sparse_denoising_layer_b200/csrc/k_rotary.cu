@@ -44,11 +44,12 @@ struct TableParams {
 };
 
 // table[p][i] = amp (cos, sin)(pos f_i).  The angle is a fixed-point count of
-// 2^-64 turns, so pos * turns wraps at whole turns by itself and far positions
-// lose nothing: the frequency's rounding, 2^-65 turns, grows with the position
-// to 2^-34 of a turn at most.  The nearest quarter turn k is taken off, and sine and cosine of
-// the rest x, |x| <= pi / 4, are their Taylor polynomials to x^9 and x^10
-// (the next terms are below 2e-9); k mod 4 swaps and negates them.
+// 2^-64 turns, so pos * turns wraps at whole turns by itself.  A frequency is right
+// to a unit or two, which a position of 2^31 makes 2^-32 of a turn, and the
+// product is cut to its upper 32 bits: 2^-31 of a turn (3e-9 rad) in all at any
+// position.  The nearest quarter turn k is taken off, and sine and cosine of the rest
+// x, |x| <= pi / 4, are their Taylor polynomials to x^9 and x^10 (the next terms
+// are below 2e-9).  k mod 4 swaps and negates them.
 //
 // A thread keeps two planes and walks over the rows of its block's share: one
 // position and one address serve both, and the polynomials run on packed
