@@ -803,26 +803,32 @@ hsa_status hsa_rope_table(hsa_ctx* ctx, const hsa_rope_cfg* cfg, const int32_t* 
   if (P == 0) return HSA_OK;
   HSA_CHECK_PTR(ctx, table);
   // 64 bits of mantissa: a frequency's error grows with the position, and a
-  // double's (2^-56 turns) would pass fp32's at positions near 2^31.
-  constexpr long double kTwoPi = 6.283185307179586476925286766559005768L;
-  const long double factor = c.factor, fast = c.fast, slow = c.slow;
+  // double's (2^-56 turns) would pass fp32's at positions near 2^31.  Plane 8 a + b is
+  // the product of two powers, a few of which serve all planes (64 calls of powl
+  // took 25 us, these 2).
+  constexpr long double kTurns = 0x1p64L / 6.283185307179586476925286766559005768L;
+  const long double factor = c.factor, slow = c.slow, span = c.fast - slow;
   hsa::RopeFreqs f{};
   f.half = rot / 2;
   f.n_axes = c.n_axes;
   f.amp = static_cast<float>(c.amp);
   for (int x = 0, j = 0; x < c.n_axes; ++x) {
     const long double dim = c.dims[x];
-    const long double base = c.scaling == HSA_ROPE_BASE && dim > 2.0L
-                                 ? c.base * powl(factor, dim / (dim - 2.0L)) : c.base;
-    for (int i = 0; i < c.dims[x] / 2; ++i, ++j) {
-      long double w = powl(base, -2.0L * i / dim);
+    long double lg = log2l(c.base);
+    if (c.scaling == HSA_ROPE_BASE && dim > 2.0L) lg += log2l(factor) * dim / (dim - 2.0L);
+    long double ones[8], eights[8];
+    const int half = c.dims[x] / 2;
+    for (int i = 0; i < 8 && i < half; ++i) ones[i] = exp2l(-2 * i * lg / dim);
+    for (int i = 0; 8 * i < half; ++i) eights[i] = exp2l(-16 * i * lg / dim);
+    for (int i = 0; i < half; ++i, ++j) {
+      long double w = ones[i & 7] * eights[i >> 3];
       if (c.scaling == HSA_ROPE_LINEAR) w /= factor;
       if (c.scaling == HSA_ROPE_PARTS) {
-        long double keep = (c.orig_len * w / kTwoPi - slow) / (fast - slow);
+        long double keep = (c.orig_len * w * (kTurns / 0x1p64L) - slow) / span;
         keep = keep < 0.0L ? 0.0L : keep > 1.0L ? 1.0L : keep;
         w = (1.0L - keep) * w / factor + keep * w;
       }
-      f.turns[j] = static_cast<uint64_t>(llrintl(ldexpl(w / kTwoPi, 64)));  // w <= 1
+      f.turns[j] = static_cast<uint64_t>(llrintl(w * kTurns));  // w <= 1
       f.axis[j] = static_cast<uint8_t>(x);
     }
   }
