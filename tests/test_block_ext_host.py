@@ -1,0 +1,56 @@
+"""Block extensions in the binding, on the host (no GPU): tensors by their
+attributes only, as the binding looks at them."""
+
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from token_sparse_denoising_layer_b200 import abi  # noqa: E402
+
+D, N = 128, 8
+
+
+class OnDevice:
+    """What the binding asks a tensor, of one that would lie on CUDA device `where`."""
+
+    def __init__(self, *shape, dtype=torch.float32, where=0):
+        self.shape, self.dtype, self.where, self.is_cuda = torch.Size(shape), dtype, where, True
+
+    def get_device(self):
+        return self.where
+
+    def numel(self):
+        return self.shape.numel()
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+    def view(self, dtype):
+        return OnDevice(*self.shape, dtype=dtype, where=self.where)
+
+
+def _ctx():
+    return types.SimpleNamespace(ptr=None, cfg=abi.hsa_model_cfg(N, 16, D, 1, 64, 1), device=0)
+
+
+def _xa(where=0):
+    t = lambda *s: OnDevice(*s, dtype=torch.bfloat16, where=where)  # noqa: E731
+    return abi.cross_attn(t(D, D), t(D, D), t(5, D), t(5, D), 5)
+
+
+def test_a_bool_text_mask_is_taken_as_cross_attention_takes_one():
+    for dtype in (torch.bool, torch.uint8):
+        s = abi.block_ext(xa=_xa(), txt_mask=OnDevice(5, dtype=dtype))
+        assert s.txt_mask == 4096
+    with pytest.raises(ValueError, match="txt_mask"):
+        abi.block_ext(xa=_xa(), txt_mask=OnDevice(4, dtype=torch.bool))
+    with pytest.raises(ValueError, match="txt_mask"):
+        abi.block_ext(xa=_xa(), txt_mask=OnDevice(5, dtype=torch.int32))

@@ -668,8 +668,11 @@ def block_ext(mod=None, xa: Optional[hsa_cross_attn] = None, txt_len=None, txt_m
               wq: Optional[hsa_layer_weights_quant] = None) -> hsa_block_ext:
     """What a block has beyond hsa_layer_forward (include/hsa.h); keeps its parts alive.
 
-    mod: device fp32 [6, D]; txt_len: device int32 [1]; txt_mask: device uint8 [n_txt]."""
+    mod: device fp32 [6, D]; txt_len: device int32 [1]; txt_mask: device uint8 or bool [n_txt]."""
     n_txt = 0 if xa is None else xa.n_txt
+    if txt_mask is not None and _dtype(txt_mask) == "bool":
+        import torch
+        txt_mask = txt_mask.view(torch.uint8)
     s = hsa_block_ext(_typed(None, mod, 1, "float32", "mod"),
                       ctypes.pointer(xa) if xa is not None else None,
                       _typed(None, txt_len, 1, "int32", "txt_len"),
