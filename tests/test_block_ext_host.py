@@ -54,3 +54,15 @@ def test_a_bool_text_mask_is_taken_as_cross_attention_takes_one():
         abi.block_ext(xa=_xa(), txt_mask=OnDevice(4, dtype=torch.bool))
     with pytest.raises(ValueError, match="txt_mask"):
         abi.block_ext(xa=_xa(), txt_mask=OnDevice(5, dtype=torch.int32))
+
+
+def test_structs_that_the_caller_filled_are_taken():
+    """Their tensors are not known, so only what the library checks is checked."""
+    ctx = _ctx()
+    abi._check_ext(ctx, abi.hsa_block_ext())
+    abi._check_ext(ctx, abi.hsa_block_ext(mod=4096))
+    quant = abi.hsa_layer_weights_quant(*[4096] * 8)
+    abi._check_ext(ctx, abi.block_ext(qk=abi.hsa_qk_rope(eps=1e-6), wq=quant, xa=abi.hsa_cross_attn(*[4096] * 4, 5)))
+    for short in (abi.hsa_qk_rope(table=4096, P=N - 1, rot=16), abi.qk_rope(table=OnDevice(N - 1, 8, 2), P=N - 1, rot=16)):
+        with pytest.raises(ValueError, match="row per token"):
+            abi._check_ext(ctx, abi.block_ext(qk=short))

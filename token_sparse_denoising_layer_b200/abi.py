@@ -684,7 +684,9 @@ def block_ext(mod=None, xa: Optional[hsa_cross_attn] = None, txt_len=None, txt_m
 
 
 def _check_ext(ctx: Context, ext: hsa_block_ext) -> None:
-    mod, xa, _, _, qk, wq = ext._keep
+    """The struct's tensors against the context that is to use them (those that are
+    known: a struct that the caller filled has addresses only)."""
+    mod, xa, _, _, qk, wq = getattr(ext, "_keep", (None,) * 6)
     D, F = ctx.cfg.D, ctx.cfg.F
     if mod is not None and mod.numel() < 6 * D:
         raise ValueError(f"mod needs [6, {D}] elements, has {mod.numel()}")
@@ -693,7 +695,7 @@ def _check_ext(ctx: Context, ext: hsa_block_ext) -> None:
         if qk.table is not None and qk.P < ctx.cfg.N:
             raise ValueError(f"a block's rotary table needs a row per token: {ctx.cfg.N}, has {qk.P}")
     if wq is not None:
-        for (q, _), shape in zip(wq._keep, ((3 * D, D), (D, D), (F, D), (D, F))):
+        for (q, _), shape in zip(getattr(wq, "_keep", ()), ((3 * D, D), (D, D), (F, D), (D, F))):
             if tuple(q.shape) != shape:
                 raise ValueError(f"8-bit block weights need shape {shape}, have {tuple(q.shape)}")
 
