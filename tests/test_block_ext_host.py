@@ -66,3 +66,19 @@ def test_structs_that_the_caller_filled_are_taken():
     for short in (abi.hsa_qk_rope(table=4096, P=N - 1, rot=16), abi.qk_rope(table=OnDevice(N - 1, 8, 2), P=N - 1, rot=16)):
         with pytest.raises(ValueError, match="row per token"):
             abi._check_ext(ctx, abi.block_ext(qk=short))
+
+
+@pytest.mark.parametrize("what", ["mod", "txt_len", "txt_mask", "xa", "wq"])
+def test_tensors_of_another_device_are_refused(what):
+    quant = abi.hsa_layer_weights_quant(*[4096] * 8)
+
+    def ext(where):
+        i8 = lambda *s: (OnDevice(*s, dtype=torch.int8, where=where), OnDevice(s[0], where=where))  # noqa: E731
+        quant._keep = [i8(3 * D, D), i8(D, D), i8(64, D), i8(D, 64)]
+        parts = {"mod": OnDevice(6, D, where=where), "txt_len": OnDevice(1, dtype=torch.int32, where=where),
+                 "txt_mask": OnDevice(5, dtype=torch.uint8, where=where), "xa": _xa(where), "wq": quant}
+        return abi.block_ext(**{"xa": _xa(), **{what: parts[what]}})
+
+    abi._check_ext(_ctx(), ext(0))
+    with pytest.raises(ValueError, match="on cuda:1, the context on cuda:0"):
+        abi._check_ext(_ctx(), ext(1))

@@ -686,18 +686,23 @@ def block_ext(mod=None, xa: Optional[hsa_cross_attn] = None, txt_len=None, txt_m
 def _check_ext(ctx: Context, ext: hsa_block_ext) -> None:
     """The struct's tensors against the context that is to use them (those that are
     known: a struct that the caller filled has addresses only)."""
-    mod, xa, _, _, qk, wq = getattr(ext, "_keep", (None,) * 6)
+    mod, xa, txt_len, txt_mask, qk, wq = getattr(ext, "_keep", (None,) * 6)
     D, F = ctx.cfg.D, ctx.cfg.F
+    pairs = getattr(wq, "_keep", ())  # 8-bit weights and their scales
+    for t, what in [(mod, "mod"), (txt_len, "txt_len"), (txt_mask, "txt_mask"),
+                    *((t, "a cross-attention tensor") for t in getattr(xa, "_keep", ())),
+                    *((t, "an 8-bit weight or scale") for pair in pairs for t in pair)]:
+        if t is not None:
+            _on_device(ctx, t, what)
     if mod is not None and mod.numel() < 6 * D:
         raise ValueError(f"mod needs [6, {D}] elements, has {mod.numel()}")
     if qk is not None:
         _check_qk(ctx, qk)
         if qk.table is not None and qk.P < ctx.cfg.N:
             raise ValueError(f"a block's rotary table needs a row per token: {ctx.cfg.N}, has {qk.P}")
-    if wq is not None:
-        for (q, _), shape in zip(getattr(wq, "_keep", ()), ((3 * D, D), (D, D), (F, D), (D, F))):
-            if tuple(q.shape) != shape:
-                raise ValueError(f"8-bit block weights need shape {shape}, have {tuple(q.shape)}")
+    for (q, _), shape in zip(pairs, ((3 * D, D), (D, D), (F, D), (D, F))):
+        if tuple(q.shape) != shape:
+            raise ValueError(f"8-bit block weights need shape {shape}, have {tuple(q.shape)}")
 
 
 def hsa_layer_forward_ext(ctx: Context, w: Optional[hsa_layer_weights],
