@@ -82,3 +82,19 @@ def test_tensors_of_another_device_are_refused(what):
     abi._check_ext(_ctx(), ext(0))
     with pytest.raises(ValueError, match="on cuda:1, the context on cuda:0"):
         abi._check_ext(_ctx(), ext(1))
+
+
+def test_modulation_and_norm_weights_of_another_shape_are_refused():
+    ctx = _ctx()
+    for shape in ((6, D), (6 * D,), (1, 6, D), (7, D)):
+        abi._check_ext(ctx, abi.block_ext(mod=OnDevice(*shape)))
+    for shape in ((6, 2 * D), (5, D), (6, 1, 2 * D)):
+        with pytest.raises(ValueError, match="mod needs"):
+            abi._check_ext(ctx, abi.block_ext(mod=OnDevice(*shape)))
+    two = types.SimpleNamespace(ptr=None, cfg=abi.hsa_model_cfg(N, 16, D, 2, 64, 1), device=0)
+    for norm, width in (("head", D // 2), ("row", D)):
+        abi._check_qk(two, abi.qk_rope(norm=norm, w_q=OnDevice(width), w_k=OnDevice(1, width)))
+        for bad in (width // 2, width + 4, 2 * width):
+            with pytest.raises(ValueError, match=f"norm weights need {width}"):
+                abi._check_qk(two, abi.qk_rope(norm=norm, w_k=OnDevice(bad)))
+    abi._check_qk(two, abi.qk_rope(norm="none", w_q=OnDevice(3)))

@@ -580,7 +580,7 @@ def _check_qk(ctx: Context, a: hsa_qk_rope) -> None:
     if a.norm:
         width = ctx.cfg.D if a.norm == 2 else ctx.cfg.D // ctx.cfg.H
         for have in getattr(a, "_widths", ()):
-            if have < width:
+            if have != width:  # (weights of a row given for heads would be read as the first head's)
                 raise ValueError(f"norm weights need {width} elements, have {have}")
     for where in getattr(a, "_devices", ()):
         if ctx.device is not None and where != ctx.device:
@@ -694,8 +694,8 @@ def _check_ext(ctx: Context, ext: hsa_block_ext) -> None:
                     *((t, "an 8-bit weight or scale") for pair in pairs for t in pair)]:
         if t is not None:
             _on_device(ctx, t, what)
-    if mod is not None and mod.numel() < 6 * D:
-        raise ValueError(f"mod needs [6, {D}] elements, has {mod.numel()}")
+    if mod is not None and (mod.numel() < 6 * D or mod.dim() > 1 and mod.shape[-1] != D):
+        raise ValueError(f"mod needs rows [6, {D}], has {tuple(mod.shape)}")
     if qk is not None:
         _check_qk(ctx, qk)
         if qk.table is not None and qk.P < ctx.cfg.N:
