@@ -610,7 +610,8 @@ typedef struct {
 /*
  * o[m] = sum_j softmax_j(scale q[m] . k[b][j]) v[b][j] per head, over the keys
  * j < kv_len[b] that kv_mask[b] lets through; b is the sequence of row m.  Statistics and sums in
- * fp32.  A row without any key gets zeros.  What lies in unseen keys and values (NaN,
+ * fp32; the weights fp32 where sequences have few queries on average (n (H / kv_heads) <= 4 B),
+ * else rounded to bf16 for their product with v.  A row without any key gets zeros.  What lies in unseen keys and values (NaN,
  * infinities) never reaches the result.  Rows of no sequence are left as they were.
  * q_start, kv_len and kv_mask are read on the device, so a captured graph
  * serves later prompts of other lengths.  A kv_len outside [0, S] is clamped, a q_start

@@ -8,7 +8,10 @@
 // Arithmetic of a tile as in the active-query attention (k_attn.cu): two
 // tiles of 128 rows share every 128-key tile, S and O live in TMEM,
 // P is written over S as bf16 and read from there by the second product, and
-// the two query tiles ping-pong.  What differs:
+// the two query tiles ping-pong.  P is rounded because that product takes both operands
+// in V's type; the row sums add it unrounded in fp32.  A weight is off by 2^-8 of
+// itself at most: 2.2e-3 of the output's norm against 64 bits, 1.7e-3 of it
+// the output's own rounding.  What differs:
 //  - A row is a query and a head: where several query heads share a key head, some
 //    of them may lie side by side in a tile (launch_hd says when), so that short
 //    sequences fill it.
@@ -28,7 +31,8 @@
 //  - Key tiles before the first and after the last seen key are not loaded.
 //    In tiles with unseen keys the scores are replaced by -inf and the unseen
 //    rows of V are zeroed in shared memory before the product reads them: a
-//    weight of 0 would not silence a NaN there.
+//    weight of 0 would not silence a NaN there.  (8190 queries, 4096 keys, 12 heads of
+//    4 x 128: 195 us without a mask, 199 with all keys seen, 232 with a tenth unseen.)
 //  - Rows without any key get zeros.  Warps whose 32 rows lie past the
 //    sequence's end (one query a sequence) do no softmax.
 //

@@ -10,9 +10,9 @@
 // Bound by HBM: a row is read once into registers, reduced, and written.  A
 // row is owned by a warp, or by 128 or 512 threads when a warp's registers
 // would not hold it.  What covers the latency is rows in flight, so the register count is
-// capped (K = 8960: 145 us with five blocks of 128 threads an SM, 172 with 256
-// threads a row).  32760 rows of bf16: K = 1536 26 us (5.7 TB/s),
-// K = 8960 126 us (7.0 TB/s, part of the bytes still being in L2 when the product reads them).
+// capped to what lets seven blocks of 128 threads share an SM.  32760 rows of bf16:
+// K = 1536 27 us (5.5 TB/s), K = 8960 128 us (6.9 TB/s; 141 with five blocks, 185
+// with 256 threads a row).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
